@@ -259,6 +259,148 @@ qs_status qstate_decode_step_batch(qstate_handle* h, const qstate_tensors* pool,
 qs_status qstate_dequantize(qstate_handle* h, const qstate_tensors* src, float* S,
                             void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the decode step: what turns a prompt into a state and moves states
+ * between slots.  Conventions as above: asynchronous on `stream`, nothing
+ * allocated, no synchronization, so every call may be captured into a graph.
+ * Rows are addressed by a stride in elements between tokens (a tensor may be
+ * a slice of a wider one); within a row heads and channels are contiguous.
+ * `offsets`: device int32 [n+1], not decreasing; sequence i is the tokens
+ * offsets[i] .. offsets[i+1]-1 of a packed [tokens, ...] tensor (it may have
+ * none).  Tokens outside offsets[0] .. offsets[n] are neither read for a
+ * result nor written.  Outputs must not overlap inputs except where said.
+ * ------------------------------------------------------------------------ */
+
+/* Short causal convolution of each channel with the `width` last tokens:
+ *   out[t][c] = act(bias[c] + sum_j weight[j][c] x[t-(width-1)+j][c]),
+ * act(y) = y / (1 + e^-y) when silu, else y; sums in fp32.  The rows before a
+ * sequence's first token are its window: the last width-1 rows it has seen,
+ * oldest first (all zeros = nothing seen).  The call replaces the window by
+ * the new last width-1 rows. */
+typedef struct {
+  const void* x;          /* [tokens][channels] in dtype */
+  void* out;              /* [tokens][channels] in dtype; must not overlap x */
+  const float* weight;    /* fp32 [width][channels] */
+  const float* bias;      /* fp32 [channels] or NULL (= 0) */
+  void* window;           /* [slots][width-1][channels] in dtype, read and written; prompts:
+                             NULL = sequences begin with zeros and keep no window */
+  const int32_t* slot;    /* device int32 [n]: sequence i's window (NULL = i); a sequence whose
+                             slot lies outside [0, slots) is skipped (no output, no window); two
+                             sequences with the same slot race */
+  const int32_t* offsets; /* prompts: see above; step: unused */
+  int64_t x_stride, out_stride;
+  int32_t dtype;          /* QS_BF16 or QS_FP32 */
+  int32_t tokens;         /* prompts: rows of x; step: unused (n rows) */
+  int32_t channels;       /* >= 1 */
+  int32_t width;          /* 2, 3 or 4 */
+  int32_t n;              /* sequences (>= 0) */
+  int32_t slots;          /* windows in the pool */
+  int32_t silu;           /* 1 or 0 */
+} qstate_conv;
+
+/* Packed prompts.  Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_causal_conv(const qstate_conv* c, void* stream);
+
+/* One token for each of n sequences: row i of x belongs to window slot[i].
+ * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_causal_conv_step(const qstate_conv* c, void* stream);
+
+typedef enum { QS_NORM_NONE = 0, QS_NORM_L2 = 1, QS_NORM_RMS = 2 } qs_norm;
+
+/* Norm of each query and key head and the rotation by position, in one pass:
+ *   L2:  y = x / sqrt(sum x^2 + eps);  RMS: y = x / sqrt(mean x^2 + eps) * weight;
+ *   pairs of y's first `rot` channels turn by position * frequency[pair]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos), pairs (i, i + rot/2), or
+ *   (2i, 2i+1) when interleaved;  q_out = y q_scale, k_out = y.
+ * fp32 throughout, the angle in fp64. */
+typedef struct {
+  const void* q;            /* [tokens][q_heads][dim] in dtype */
+  const void* k;            /* [tokens][k_heads][dim] (NULL with k_heads 0) */
+  void* q_out;              /* may be q itself (same stride), else must not overlap */
+  void* k_out;
+  const float* q_weight;    /* fp32 [dim] or NULL (= 1); RMS only */
+  const float* k_weight;
+  const int32_t* position;  /* device int32 [tokens] (rot > 0) */
+  const double* frequency;  /* device fp64 [rot/2], radians per position (rot > 0) */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* every row 16-byte aligned */
+  int32_t dtype;            /* QS_BF16 or QS_FP32 */
+  int32_t tokens, q_heads, k_heads;
+  int32_t dim;              /* a multiple of 8, 8..512 */
+  int32_t rot;              /* rotated channels: 0 or a multiple of 16, at most dim */
+  int32_t norm;             /* qs_norm */
+  int32_t interleaved;
+  float eps;                /* >= 0 */
+  float q_scale;
+} qstate_qk;
+
+/* Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_qk_norm_rotate(const qstate_qk* a, void* stream);
+
+/* Scan of n packed prompts with the handle's recurrence (kind, decay mode, H,
+ * dk, dv, in_dtype; the stored format does not matter) [LoReS, PU]: for each
+ * sequence the steps of the decode recurrence above over its tokens, from
+ * `initial`, in fp32 and without requantization.
+ *   q, k: [tokens][k_heads][dk], v and out: [tokens][H][dv] in in_dtype; heads
+ *   h*k_heads/H .. share a query and key head (k_heads divides H).
+ *   out = S q (+ skip[h] v); final = the state after the last token (what
+ *   qstate_quantize takes), or `initial` for a sequence of no tokens.
+ * decay must not be negative. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* decay;      /* fp32 [tokens][H] or [tokens][H][dk] */
+  const float* beta;       /* fp32 [tokens][H] or NULL (= 1) */
+  const float* skip;       /* fp32 [H] or NULL (= 0) */
+  const float* initial;    /* fp32 [n][H][dv][dk] or NULL (= 0) */
+  float* final;            /* fp32 [n][H][dv][dk]; may be `initial` */
+  void* out;               /* must not overlap q, k or v */
+  const int32_t* offsets;  /* NULL: one sequence of all tokens (n = 1) */
+  int64_t q_stride, k_stride, v_stride, decay_stride, beta_stride, out_stride;
+  int32_t tokens, n, k_heads;
+} qstate_scan_args;
+
+/* Device bytes qstate_scan needs as its workspace for these arguments (only
+ * tokens, n and k_heads are read); may be 0.  Host only. */
+qs_status qstate_scan_workspace(const qstate_handle* h, const qstate_scan_args* a, uint64_t* bytes);
+
+/* `workspace`: device memory of at least that size, 256-byte aligned, used
+ * by this call alone until it has finished on `stream` (NULL when 0 bytes).
+ * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* a, void* workspace, uint64_t bytes,
+                      void* stream);
+
+/* A buffer that has `bytes` bytes for each slot, next to a state's own
+ * buffers (a convolution's windows). */
+typedef struct {
+  const void* src;
+  void* dst;
+  uint64_t bytes;
+} qstate_slot_buffer;
+
+/* Copy whole state slots: for i < n, slot dst_slot[i] of `pool` (the handle's
+ * B slots) becomes slot src_slot[i] of `source` (src_slots slots of the same
+ * configuration; may be the pool itself), or all zeros (the state S = 0) when
+ * src_slot[i] is -1.  Forks (one source, many destinations), moves, clears,
+ * and hands states from one pool to another in one launch.  Elements with a
+ * slot out of range are skipped.  Destinations must be distinct, and within
+ * one pool no destination may be another element's source (such elements
+ * race).  extra: up to 6 more buffers of both pools.
+ * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_copy_slots(qstate_handle* h, const qstate_tensors* pool, const qstate_tensors* source,
+                            int32_t src_slots, int32_t n, const int32_t* src_slot, const int32_t* dst_slot,
+                            const qstate_slot_buffer* extra, int32_t n_extra, void* stream);
+
+/* Compact a pool in place: with F = the number of nonzero live[b], the i-th
+ * live slot at or behind F moves to the i-th free slot before F; the other
+ * live slots stay.  where[b] = the slot that slot b's state is in now, -1 for
+ * a free slot b.  Slots from F on keep stale bytes.  B <= 16384.
+ *   live: device uint8 [B]; where: device int32 [B]; extra as above (src = dst).
+ * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+qs_status qstate_compact_slots(qstate_handle* h, const qstate_tensors* pool, const uint8_t* live,
+                               int32_t* where, const qstate_slot_buffer* extra, int32_t n_extra,
+                               void* stream);
+
 /* Decay-based mixed precision map [LoReS]: within each of `groups` groups
  * of `per_group` units (heads, or key channels of one head), mark the
  * floor(frac*per_group + 0.5) units with the smallest decay-rate statistic

@@ -21,11 +21,15 @@ DTYPE = {"fp32": 0, "bf16": 1, "fp16": 2}
 MAP = {"none": 0, "head": 1, "key": 2}
 ROUNDING = {"nearest": 0, "stochastic": 1}
 AXIS = {"value": 0, "key": 1, "head": 2}
+NORM = {"none": 0, "l2": 1, "rms": 2}
+MAX_EXTRA = 6      # extra per-slot buffers of a slot copy
 
 EXPORTS = (
     "qstate_plan", "qstate_init", "qstate_quantize", "qstate_decode_step", "qstate_decode_step_batch",
     "qstate_dequantize", "qstate_build_map", "qstate_destroy", "qstate_strerror",
     "qstate_last_error", "qstate_kernel_name",
+    "qstate_causal_conv", "qstate_causal_conv_step", "qstate_qk_norm_rotate", "qstate_scan_workspace", "qstate_scan",
+    "qstate_copy_slots", "qstate_compact_slots",
 )
 
 
@@ -58,6 +62,34 @@ class Inputs(ctypes.Structure):
                 ("decay", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
 
 
+_VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class Conv(ctypes.Structure):
+    _fields_ = [("x", _VP), ("out", _VP), ("weight", _VP), ("bias", _VP), ("window", _VP), ("slot", _VP),
+                ("offsets", _VP), ("x_stride", _I64), ("out_stride", _I64), ("dtype", _I32), ("tokens", _I32),
+                ("channels", _I32), ("width", _I32), ("n", _I32), ("slots", _I32), ("silu", _I32)]
+
+
+class Qk(ctypes.Structure):
+    _fields_ = [("q", _VP), ("k", _VP), ("q_out", _VP), ("k_out", _VP), ("q_weight", _VP), ("k_weight", _VP),
+                ("position", _VP), ("frequency", _VP), ("q_stride", _I64), ("k_stride", _I64),
+                ("q_out_stride", _I64), ("k_out_stride", _I64), ("dtype", _I32), ("tokens", _I32),
+                ("q_heads", _I32), ("k_heads", _I32), ("dim", _I32), ("rot", _I32), ("norm", _I32),
+                ("interleaved", _I32), ("eps", ctypes.c_float), ("q_scale", ctypes.c_float)]
+
+
+class Scan(ctypes.Structure):
+    _fields_ = [("q", _VP), ("k", _VP), ("v", _VP), ("decay", _VP), ("beta", _VP), ("skip", _VP), ("initial", _VP),
+                ("final", _VP), ("out", _VP), ("offsets", _VP), ("q_stride", _I64), ("k_stride", _I64),
+                ("v_stride", _I64), ("decay_stride", _I64), ("beta_stride", _I64), ("out_stride", _I64),
+                ("tokens", _I32), ("n", _I32), ("k_heads", _I32)]
+
+
+class SlotBuffer(ctypes.Structure):
+    _fields_ = [("src", _VP), ("dst", _VP), ("bytes", ctypes.c_uint64)]
+
+
 class QStateError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         super().__init__(f"{where}: status {status} ({detail})")
@@ -85,6 +117,16 @@ def lib() -> ctypes.CDLL:
         L.qstate_decode_step_batch.argtypes = [vp, P(Tensors), P(Inputs), vp, ctypes.c_int32, vp, vp, vp]
         L.qstate_dequantize.argtypes = [vp, P(Tensors), vp, vp]
         L.qstate_build_map.argtypes = [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, vp]
+        L.qstate_causal_conv.argtypes = [P(Conv), vp]
+        L.qstate_causal_conv_step.argtypes = [P(Conv), vp]
+        L.qstate_qk_norm_rotate.argtypes = [P(Qk), vp]
+        L.qstate_scan_workspace.argtypes = [vp, P(Scan), P(ctypes.c_uint64)]
+        L.qstate_scan.argtypes = [vp, P(Scan), vp, ctypes.c_uint64, vp]
+        L.qstate_copy_slots.argtypes = [vp, P(Tensors), P(Tensors), _I32, _I32, vp, vp, P(SlotBuffer), _I32, vp]
+        L.qstate_compact_slots.argtypes = [vp, P(Tensors), vp, vp, P(SlotBuffer), _I32, vp]
+        for f in ("qstate_causal_conv", "qstate_causal_conv_step", "qstate_qk_norm_rotate", "qstate_scan_workspace",
+                  "qstate_scan", "qstate_copy_slots", "qstate_compact_slots"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("qstate_plan", "qstate_init", "qstate_quantize", "qstate_decode_step",
                   "qstate_decode_step_batch", "qstate_dequantize", "qstate_build_map"):
             getattr(L, f).restype = ctypes.c_int

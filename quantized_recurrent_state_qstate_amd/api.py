@@ -141,6 +141,39 @@ def check_inputs(cfg: "StateConfig", n: int, device, q, k, v, decay, beta, out) 
     check_tensor("out", out, torch.float32, nh * cfg.dv, device)
 
 
+def check_rows(name: str, t, dtype, shape, device) -> int:
+    """A tensor of `shape` whose rows (all dimensions but the first) are
+    contiguous, at any stride between them; returns that stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    width = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: rows are not contiguous")
+        width *= size
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    stride = t.stride(0)
+    if t.shape[0] > 1 and stride < width:
+        raise ValueError(f"{name}: rows overlap (stride {stride} of {width})")
+    return stride if t.shape[0] > 1 else width
+
+
+def _empty(shape, dtype, device, stream):
+    """Uninitialised memory for a call on `stream` (None: the current one): taken
+    on that stream, so that its reuse waits for the call."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class QState:
     """A libqstate handle for one configuration on the current HIP device."""
 
@@ -254,3 +287,137 @@ class QState:
                                                        _ptr(slot), _ptr(step), self._stream(stream)),
                    "qstate_decode_step_batch")
         return out
+
+    def scan(self, q, k, v, decay, beta=None, *, offsets=None, initial=None, final=None, skip=None, out=None,
+             stream=None):
+        """Run packed prompts through the recurrence: (out, final).
+
+        q, k [T,G,dk] and v [T,H,dv] in the configured input dtype (heads
+        h*G//H .. share a query and key head), decay fp32 [T,H] (or [T,H,dk]),
+        beta fp32 [T,H] or None; each may be a slice of a wider tensor whose
+        trailing dimensions are contiguous.  offsets int32 [n+1] on the device:
+        sequence i is tokens offsets[i]..offsets[i+1]-1 (None: one sequence);
+        tokens outside every sequence are left as they were in `out`.
+        initial fp32 [n,H,dv,dk] or None (zeros); skip fp32 [H] adds skip[h] v
+        to the output.  out [T,H,dv] in the input dtype; final fp32
+        [n,H,dv,dk] is what `quantize` takes, and may be `initial` itself."""
+        import torch
+        c = self.cfg
+        dev = self.device
+        ind = torch.bfloat16 if c.in_dtype == "bf16" else torch.float32
+        if not isinstance(v, torch.Tensor) or v.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k and v must be [T, heads, dim] tensors")
+        T, G = v.shape[0], k.shape[1]
+        n = 1
+        if offsets is not None:
+            if not isinstance(offsets, torch.Tensor) or offsets.numel() < 1:
+                raise ValueError("offsets must be an int32 tensor [n+1]")
+            n = offsets.numel() - 1
+            check_tensor("offsets", offsets, torch.int32, n + 1, dev)
+        a = _lib.Scan()
+        a.q_stride = check_rows("q", q, ind, (T, G, c.dk), dev)
+        a.k_stride = check_rows("k", k, ind, (T, G, c.dk), dev)
+        a.v_stride = check_rows("v", v, ind, (T, c.H, c.dv), dev)
+        a.decay_stride = check_rows("decay", decay, torch.float32,
+                                    (T, c.H, c.dk) if c.decay_mode == "key" else (T, c.H), dev)
+        if beta is not None:
+            a.beta_stride = check_rows("beta", beta, torch.float32, (T, c.H), dev)
+            a.beta = beta.data_ptr()
+        if skip is not None:
+            check_tensor("skip", skip, torch.float32, c.H, dev)
+            a.skip = skip.data_ptr()
+        state = n * c.H * c.dv * c.dk
+        if initial is not None:
+            check_tensor("initial", initial, torch.float32, state, dev)
+            a.initial = initial.data_ptr()
+        if out is None:
+            out = _empty((T, c.H, c.dv), ind, dev, stream)
+        a.out_stride = check_rows("out", out, ind, (T, c.H, c.dv), dev)
+        if final is None:
+            final = _empty((n, c.H, c.dv, c.dk), torch.float32, dev, stream)
+        else:
+            check_tensor("final", final, torch.float32, state, dev)
+        a.q, a.k, a.v, a.decay = q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr()
+        a.out, a.final, a.offsets = out.data_ptr(), final.data_ptr(), _ptr(offsets)
+        a.tokens, a.n, a.k_heads = T, n, G
+        L = _lib.lib()
+        need = ctypes.c_uint64()
+        _lib.check(L.qstate_scan_workspace(self._h, ctypes.byref(a), ctypes.byref(need)), "qstate_scan_workspace")
+        # the call's own: a captured call keeps it in its graph's memory
+        ws = _empty((need.value,), torch.uint8, dev, stream) if need.value else None
+        _lib.check(L.qstate_scan(self._h, ctypes.byref(a), _ptr(ws), need.value, self._stream(stream)), "qstate_scan")
+        return out, final
+
+    def _slot_bytes(self, st: dict, name: str) -> int:
+        return self.sizes[name] // self.cfg.B if self.cfg.B else 0
+
+    def _extra(self, extra, source_extra, src_slots: int):
+        """Per-slot buffers that go along: tensors [slots, ...], contiguous, on this device."""
+        import torch
+        src = list(extra if source_extra is None else source_extra)
+        dst = list(extra)
+        if len(src) != len(dst) or len(dst) > _lib.MAX_EXTRA:
+            raise ValueError(f"{len(dst)} extra buffers and {len(src)} of the source (at most {_lib.MAX_EXTRA})")
+        bufs = (_lib.SlotBuffer * max(1, len(dst)))()
+        for i, (s, d) in enumerate(zip(src, dst)):
+            for t, slots in ((d, self.cfg.B), (s, src_slots)):
+                if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.shape[0] < slots or not t.is_contiguous():
+                    raise ValueError(f"extra[{i}]: expected a contiguous tensor of at least {slots} slots")
+                if t.device != self.device:
+                    raise ValueError(f"extra[{i}]: on {t.device}, expected {self.device}")
+            if s.dtype != d.dtype or s.shape[1:] != d.shape[1:]:
+                raise ValueError(f"extra[{i}]: {s.dtype} {tuple(s.shape[1:])} into {d.dtype} {tuple(d.shape[1:])}")
+            bufs[i] = _lib.SlotBuffer(s.data_ptr(), d.data_ptr(), d.element_size() * d[0].numel() if d.shape[0] else 0)
+        return bufs, len(dst)
+
+    def copy_slots(self, pool: dict, src_slot, dst_slot, *, source=None, source_slots=None, extra=(),
+                   source_extra=None, stream=None) -> None:
+        """Slot dst_slot[i] of `pool` becomes slot src_slot[i] of `source` (a
+        state of `source_slots` slots of this configuration; None: the pool
+        itself), or the zero state when src_slot[i] is -1.  src_slot, dst_slot:
+        int32 [n] on the device; elements out of range are skipped.  Forks,
+        moves, clears and hand-overs between pools in one launch.
+        Destinations must be distinct and, within one pool, must not be
+        another element's source.  extra: up to 6 more tensors [B, ...] that
+        go along (source_extra: theirs in the source)."""
+        import torch
+        n = int(src_slot.numel())
+        check_tensor("src_slot", src_slot, torch.int32, n, self.device)
+        check_tensor("dst_slot", dst_slot, torch.int32, n, self.device)
+        if source is None:
+            if source_slots is not None or source_extra is not None:
+                raise ValueError("source_slots and source_extra go with a source")
+            source, m = pool, self.cfg.B
+        else:
+            if source_slots is None:
+                raise ValueError("source_slots: the source's number of slots")
+            if extra and source_extra is None and source is not pool:
+                raise ValueError("extra buffers of another pool need source_extra")
+            m = int(source_slots)
+            check_state(self.cfg, {k: self._slot_bytes(source, k) * m for k in self.sizes}, source, self.device)
+        check_state(self.cfg, self.sizes, pool, self.device)
+        bufs, ne = self._extra(extra, source_extra, m)
+        d, s = self._tensors(pool), self._tensors(source)
+        _lib.check(_lib.lib().qstate_copy_slots(self._h, ctypes.byref(d), ctypes.byref(s), m, n, _ptr(src_slot),
+                                                _ptr(dst_slot), bufs, ne, self._stream(stream)), "qstate_copy_slots")
+
+    def compact_slots(self, pool: dict, live, *, extra=(), where=None, stream=None):
+        """Move the live slots of `pool` (live: uint8 or bool [B], device) to
+        its front: with F of them, the i-th live slot at or behind F goes to
+        the i-th free slot before F.  Returns where int32 [B]: the slot each
+        slot's state is in now, -1 for free ones.  extra: further tensors
+        [B, ...] that go along."""
+        import torch
+        c = self.cfg
+        if isinstance(live, torch.Tensor) and live.dtype == torch.bool:
+            live = live.view(torch.uint8)
+        check_tensor("live", live, torch.uint8, c.B, self.device)
+        if where is None:
+            where = _empty((c.B,), torch.int32, self.device, stream)
+        check_tensor("where", where, torch.int32, c.B, self.device)
+        check_state(c, self.sizes, pool, self.device)
+        bufs, ne = self._extra(extra, None, c.B)
+        t = self._tensors(pool)
+        _lib.check(_lib.lib().qstate_compact_slots(self._h, ctypes.byref(t), _ptr(live), _ptr(where), bufs, ne,
+                                                   self._stream(stream)), "qstate_compact_slots")
+        return where

@@ -16,6 +16,7 @@
 
 #include "qstate.h"
 #include "qstate_internal.hpp"
+#include "qstate_ops.hpp"
 
 namespace {
 
@@ -354,6 +355,23 @@ qs::Args base_args(const qstate_handle* h, const qstate_tensors* st) {
 }
 
 }  // namespace
+
+namespace qs {
+
+qs_status op_fail(qs_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+qs_status op_ok() { return ok(); }
+HandleView op_view(const qstate_handle* h) { return {&h->cfg, &h->plan.sizes}; }
+qs_status op_check_tensors(const qstate_handle* h, const qstate_tensors* st) { return check_tensors(h, st); }
+qs_status op_check_device(const qstate_handle* h) { return check_device(h); }
+
+}  // namespace qs
 
 extern "C" {
 
