@@ -94,4 +94,13 @@ struct ScanArgs {
 };
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
+// Segments of the chunked scan: cells of `seg` tokens of the packed axis,
+// cut again where sequences begin; `count` bounds their number.
+struct ScanSegs {
+  int32_t seg, count;
+  float* states;           // [count][H][dv][dk], null: no sequence is cut
+  float* total;            // [count][H] log2 of a segment's whole decay
+};
+hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
+
 }  // namespace qs

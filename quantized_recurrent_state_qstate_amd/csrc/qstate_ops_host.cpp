@@ -210,12 +210,39 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
   return QS_OK;
 }
 
+// How a scan runs.  The chunked kernels take bf16 prompts with one decay a
+// head; everything else runs token by token.  Additive sequences are cut into
+// segments when the heads alone would leave compute units idle: about 512
+// workgroups, no segment shorter than 256 tokens (each costs a state written
+// and read).
+struct ScanPlan {
+  bool chunked;
+  qs::ScanSegs segs;
+  uint64_t states, total;   // workspace bytes
+};
+static ScanPlan scan_plan(const qs::ScanArgs& a) {
+  ScanPlan p{};
+  p.chunked = a.bf16 && !a.key && a.T >= 64;
+  p.segs.seg = 1 << 30;
+  p.segs.count = a.n;
+  if (!p.chunked || a.delta) return p;
+  const int64_t work = (int64_t)a.T * a.H * ((a.dv + 63) / 64);
+  const int64_t seg = std::max<int64_t>(256, (work / 512 + 63) / 64 * 64);
+  if (seg >= a.T) return p;
+  p.segs.seg = (int32_t)seg;
+  p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);
+  p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)a.dv * (uint64_t)a.dk * 4u;
+  p.total = ((uint64_t)p.segs.count * (uint64_t)a.H * 4u + 255u) / 256u * 256u;
+  return p;
+}
+
 qs_status qstate_scan_workspace(const qstate_handle* h, const qstate_scan_args* c, uint64_t* bytes) {
   if (!bytes) return op_fail(QS_EINVAL, "bytes is NULL");
   qs::ScanArgs a{};
   qs_status s = check_scan(h, c, &a);
   if (s != QS_OK) return s;
-  *bytes = 0;
+  const ScanPlan p = scan_plan(a);
+  *bytes = p.states + p.total;
   return op_ok();
 }
 
@@ -248,8 +275,22 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
     if (overlap(r, out) || overlap(r, fin)) return op_fail(QS_EINVAL, "an output overlaps an input");
   if (overlap(out, fin) || overlap(out, ini) || (c->initial != c->final && overlap(ini, fin)))
     return op_fail(QS_EINVAL, "an output overlaps another or the initial state");
-  (void)workspace;
-  (void)bytes;
+  ScanPlan p = scan_plan(a);
+  if (p.states + p.total) {
+    if (!workspace || !aligned(workspace, 256) || bytes < p.states + p.total)
+      return op_fail(QS_EINVAL, "workspace of %llu bytes, %llu needed, 256-byte aligned", (unsigned long long)bytes,
+                     (unsigned long long)(p.states + p.total));
+    const Rows w{workspace, (int64_t)(p.states + p.total), (int64_t)(p.states + p.total), 1};
+    for (const Rows& r : ins)
+      if (overlap(r, w)) return op_fail(QS_EINVAL, "the workspace overlaps an input");
+    if (overlap(w, fin) || overlap(w, ini) || overlap(w, out))
+      return op_fail(QS_EINVAL, "the workspace overlaps an output or the initial state");
+    p.segs.total = (float*)workspace;
+    p.segs.states = (float*)((char*)workspace + p.total);
+  }
+  if ((int64_t)p.segs.count * a.H * ((a.dv + 31) / 32) > 0x7FFFFFFF ||
+      (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > 0x7FFFFFFF)
+    return op_fail(QS_EUNSUPPORTED, "%d tokens of %d sequences in one call", a.T, a.n);
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
   a.q = c->q;
   a.k = c->k;
@@ -271,7 +312,8 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   a.vec = aligned(c->q, 16) && aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->out, 16) && vw % v == 0 &&
           a.dv % v == 0 && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0 && c->v_stride % v == 0 &&
                                        c->out_stride % v == 0));
-  hipError_t e = qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
+  hipError_t e = p.chunked ? qs::launch_scan_chunk(a, p.segs, reinterpret_cast<hipStream_t>(stream))
+                           : qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));
   return op_ok();
 }

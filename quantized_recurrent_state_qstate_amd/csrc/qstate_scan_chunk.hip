@@ -1,0 +1,609 @@
+// Scan of packed bf16 prompts with one decay a head, 64 tokens at a time on
+// the matrix cores.
+//
+// With c_i the sum of log2 decays from a chunk's first token to token i and
+// S the state before the chunk,
+//   S_i = 2^{c_i} S + sum_{j<=i} 2^{c_i - c_j} u_j k_j^T,
+//   o_i = 2^{c_i} S q_i + sum_{j<=i} P_ij u_j,   P_ij = 2^{c_i - c_j} k_j.q_i,
+// and the state after the chunk is the last S_i.  Additive: u = beta v.  Delta
+// rule: u_i = beta_i (v_i - 2^{c_i} S k_i - sum_{j<i} 2^{c_i - c_j} (k_j.k_i) u_j),
+// a unit lower triangular system in the chunk's 64 rows, solved in fp32 by
+// blocks of 16: the diagonal blocks are inverted by substitution, the rest is
+// fp32 matrix instructions.
+//
+// Precision: q, k and v are bf16, so a product with one of them is exact when
+// the other operand is cut into bf16 pieces: three pieces (24 bits) of w u in
+// the state's update and of S in the delta rule's S k, two (16 bits) of S and
+// of P in the outputs, which are rounded to bf16 at the end.  All sums are fp32.
+// c is summed in fp64: differences of long sums of logs would lose the decays
+// between neighbours; a decay of zero counts as 2^-10000.
+//
+// A workgroup holds 16 NV WAVES value columns of one (segment, head): each wave
+// keeps the state of its columns in accumulators [dk][v], which are the second
+// operand of S q and S k as they are (the tiles' rows are dealt so that a lane
+// holds 8 channels in a row); k, q, v and P go through LDS.
+//
+// Segments: additive sequences may be cut at multiples of `seg` tokens.  Then
+// three launches: the state each segment adds by itself, the states between
+// segments, and the outputs; so that few long sequences fill the device.
+#include <hip/hip_runtime.h>
+
+#include "qstate_ops.hpp"
+
+namespace qs {
+namespace {
+
+using BF8 = __bf16 __attribute__((ext_vector_type(8)));
+using BF4 = __bf16 __attribute__((ext_vector_type(4)));
+using F4 = float __attribute__((ext_vector_type(4)));
+using S4 = short __attribute__((ext_vector_type(4)));
+using U4 = uint32_t __attribute__((ext_vector_type(4)));
+
+constexpr int kL = 64;   // tokens of a chunk
+
+__device__ __forceinline__ F4 mfma(BF8 a, BF8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mfma1(float a, float b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// Four rows of one column for every lane: in each group of 16 lanes, lane l
+// points at columns 4 (l & 3).. of row l >> 2 and gets column l of the rows.
+__device__ __forceinline__ BF4 read_tr(const uint16_t* p) {
+  typedef __attribute__((address_space(3))) S4* L;
+  return __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
+}
+
+// Eight floats as a sum of bf16 numbers, by cutting bits off: hi holds the
+// upper 8 significant bits, mid the next 8, lo the rest rounded.
+__device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper halves of a and b
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const __bf16 x = (__bf16)a, y = (__bf16)b;
+  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+}
+template <int N>
+__device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = f[j];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + 1 < N) {
+        d[j] = upper2(r[2 * j], r[2 * j + 1]);
+        r[2 * j] -= cut(r[2 * j]);
+        r[2 * j + 1] -= cut(r[2 * j + 1]);
+      } else {
+        d[j] = round2(r[2 * j], r[2 * j + 1]);
+      }
+    }
+    out[n] = __builtin_bit_cast(BF8, (U4){d[0], d[1], d[2], d[3]});
+  }
+}
+
+__device__ __forceinline__ BF8 join(BF4 a, BF4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Segment s of the packed tokens.  Segment s = (sequence i, cell c) with
+// s = i + c: cells are seg tokens of the packed axis, and each sequence or
+// cell boundary moves s on by one, so (i, c) follows from s and the offsets.
+struct Segment {
+  int seq, t0, t1;      // tokens
+  bool first, last, none;
+};
+__device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int s) {
+  Segment r{0, 0, 0, true, true, false};
+  int start = 0, end = a.T;
+  if (a.offsets) {
+    const int lane = (int)(threadIdx.x & 63u);
+    int lo = 0, len = a.n - 1;              // sequences i in [1, n-1] with offsets[i] / seg + i <= s
+    while (len > 0) {
+      const int step = (len + 63) >> 6;
+      const int i = lo + (lane + 1) * step;
+      const bool le = i <= lo + len && min(max(a.offsets[i], 0), a.T) / seg + i <= s;
+      const int c = (int)__popcll(__ballot(le));
+      lo += c * step;
+      len = min(len - c * step, step - 1);
+    }
+    r.seq = __builtin_amdgcn_readfirstlane(lo);
+    start = min(max(a.offsets[r.seq], 0), a.T);
+    end = min(max(a.offsets[r.seq + 1], start), a.T);
+  }
+  const int c = s - r.seq, c0 = start / seg, c1 = end > start ? (end - 1) / seg : c0;
+  r.none = c < c0 || c > c1;
+  r.first = c == c0;
+  r.last = c == c1;
+  r.t0 = r.first ? start : c * seg;
+  r.t1 = r.last ? end : (c + 1) * seg;
+  return r;
+}
+
+// 16 bytes of a bf16 row: 8 elements from column c of `width`.
+__device__ __forceinline__ U4 load8(const void* p, int64_t row, int c, int width, bool vec) {
+  const uint16_t* x = (const uint16_t*)p + row;
+  if (vec) return c < width ? *(const U4*)(x + c) : (U4){0, 0, 0, 0};
+  uint32_t d[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = c + 2 * j < width ? x[c + 2 * j] : 0u, hi = c + 2 * j + 1 < width ? x[c + 2 * j + 1] : 0u;
+    d[j] = lo | (hi << 16);
+  }
+  return (U4){d[0], d[1], d[2], d[3]};
+}
+
+__device__ __forceinline__ bool odd8(U4 u) {    // an infinity or NaN among 8 bf16 numbers
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    bad = bad || (u[j] & 0x7F80u) == 0x7F80u || (u[j] & 0x7F800000u) == 0x7F800000u;
+  return bad;
+}
+
+template <int DK, int NV, int WAVES, bool DELTA, bool OUT>
+__global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
+  constexpr int kT = 64 * WAVES;            // threads
+  constexpr int kDV = 16 * NV * WAVES;      // value columns
+  constexpr int kKS = DK / 32;              // steps of 32 channels
+  constexpr int kKR = DK + 8, kVR = kDV + 8, kPR = kL + 8, kAR = kL + 4;   // LDS rows: 16 bytes more than they need
+  constexpr int kKP = kL * DK / 8 / kT, kVP = kL * kDV / 8 / kT;           // 16-byte pieces a thread brings
+  __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR];
+  __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? kL * kKR : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[kL * kVR];           // v, then the outputs
+  __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 2 : 1][OUT ? kL * kPR : 8];   // P's two pieces
+  __shared__ __attribute__((aligned(16))) float sa[DELTA ? kL * kAR : 4];  // minus the triangle, inverted blocks
+  __shared__ double sc[kL];
+  __shared__ __attribute__((aligned(16))) float se[kL], sw[kL], sb[kL];    // 2^{c_i}, weight in the update, beta
+  __shared__ int sbad;
+
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, q4 = lane >> 4;
+  const int per = a.H * vchunks;
+  const int s = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
+  const int h = hv / vchunks, v0 = (hv % vchunks) * kDV;
+  const int kh = h / (a.H / a.G);
+  const Segment sg = find_segment(a, g.seg, s);
+  if (sg.none || (!OUT && sg.last)) return;
+  const int64_t head = (int64_t)h * a.dv;
+
+  // state tiles: row 4 q4 + r of tile 2 i + j is channel 32 i + 8 q4 + 4 j + r, column m is value v0 + ...
+  F4 S[NV][2 * kKS];
+  const int vcol = (wave * NV) * 16 + m;
+  const float* from = !OUT ? nullptr
+                      : sg.first ? (a.initial ? a.initial + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
+                                 : g.states + (int64_t)s * a.H * a.dv * DK;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int v = v0 + vcol + 16 * n;
+#pragma unroll
+    for (int t = 0; t < 2 * kKS; ++t) {
+      S[n][t] = (F4){0, 0, 0, 0};
+      if (from && v < a.dv) S[n][t] = *(const F4*)(from + (head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
+    }
+  }
+  if (OUT) {
+    // the P tiles right of the diagonal that a step of 32 tokens reads stay zero
+    for (int i = tid; i < 2 * 16 * 16; i += kT) {
+      const int b = i >> 8, r = (i >> 4) & 15, c = i & 15;
+      sp[0][(32 * b + r) * kPR + 32 * b + 16 + c] = 0;
+      sp[1][(32 * b + r) * kPR + 32 * b + 16 + c] = 0;
+    }
+  }
+
+  U4 nk[kKP], nq[OUT ? kKP : 1], nv[kVP];
+  float nd = 1.0f, nb = 0.0f;
+  auto fetch = [&](int t, int t1) {
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) {
+      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
+      const bool in = t + r < t1;
+      nk[i] = in ? load8(a.k, (int64_t)(t + r) * a.ks + (int64_t)kh * DK, c, DK, a.vec) : (U4){0, 0, 0, 0};
+      if constexpr (OUT)
+        nq[i] = in ? load8(a.q, (int64_t)(t + r) * a.qs + (int64_t)kh * DK, c, DK, a.vec) : (U4){0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+      nv[i] = t + r < t1 ? load8(a.v, (int64_t)(t + r) * a.vs + head + v0, c, a.dv - v0, a.vec) : (U4){0, 0, 0, 0};
+    }
+    nd = 1.0f;
+    nb = 0.0f;
+    if (tid < kL && t + tid < t1) {
+      nd = a.decay[(int64_t)(t + tid) * a.ds + h];
+      nb = a.beta ? a.beta[(int64_t)(t + tid) * a.bs + h] : 1.0f;
+    }
+  };
+  // The token of a chunk (behind its first) whose k, v or gates are not
+  // finite begins a chunk of its own: a product with a zero of P or of the
+  // triangle would carry it to the tokens before it.
+  auto note_bad = [&](int n) {
+    int bad = kL;
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) {
+      const int r = (i * kT + tid) / (DK / 8);
+      if (r > 0 && odd8(nk[i])) bad = min(bad, r);
+    }
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int r = (i * kT + tid) / (kDV / 8);
+      if (r > 0 && odd8(nv[i])) bad = min(bad, r);
+    }
+    if (tid > 0 && tid < kL && !(fabsf(nd) < INFINITY && fabsf(nb) < INFINITY)) bad = min(bad, tid);
+    if (bad < n) atomicMin(&sbad, bad);
+  };
+
+  if (tid == 0) sbad = kL;
+  double total = 0.0;
+  fetch(sg.t0, sg.t1);
+  __syncthreads();
+  for (int t = sg.t0; t < sg.t1;) {
+    int n = min(kL, sg.t1 - t);
+    // ---- this chunk into LDS; gates
+    note_bad(n);
+    __syncthreads();                         // sbad is known; the chunk before has been read
+    const int cutoff = sbad;
+    __syncthreads();
+    if (cutoff < n) {
+      n = cutoff;
+      fetch(t, t + n);
+      if (tid == 0) sbad = kL;
+    }
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) {
+      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
+      *(U4*)&sk[r * kKR + c] = nk[i];
+      if constexpr (OUT) *(U4*)&sq[r * kKR + c] = nq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+      *(U4*)&sv[r * kVR + c] = nv[i];
+    }
+    if (wave == 0) {
+      double c = nd == 0.0f ? -10000.0 : (double)log2f(nd);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double x = __shfl_up(c, o);
+        if (lane >= o) c += x;
+      }
+      const double all = __shfl(c, 63);
+      sc[lane] = c;
+      sb[lane] = nb;
+      se[lane] = __builtin_amdgcn_exp2f((float)c);
+      sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * (DELTA ? 1.0f : nb);
+    }
+    __syncthreads();
+    const int next = t + n;
+    if (next < sg.t1) fetch(next, sg.t1);
+    const double call = sc[kL - 1];
+    total += call;
+    const float eall = __builtin_amdgcn_exp2f((float)call);
+
+    F4 U[DELTA ? NV : 1][4];                 // u of the chunk's rows (delta rule)
+    if constexpr (OUT) {
+      // ---- P (transposed tiles: a lane gets 4 j of one i) and the triangle
+#pragma unroll
+      for (int x = 0; x < 4 / WAVES; ++x) {
+        const int it = WAVES == 4 ? wave : (x ? 3 - wave : wave);
+        const int i = 16 * it + m;
+        const double ci = sc[i];
+        for (int jt = 0; jt <= it; ++jt) {
+          F4 p = (F4){0, 0, 0, 0}, kk = (F4){0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < kKS; ++c) {
+            const BF8 kj = *(const BF8*)&sk[(16 * jt + m) * kKR + 32 * c + 8 * q4];
+            p = mfma(kj, *(const BF8*)&sq[i * kKR + 32 * c + 8 * q4], p);
+            if constexpr (DELTA) kk = mfma(kj, *(const BF8*)&sk[i * kKR + 32 * c + 8 * q4], kk);
+          }
+          const int j = 16 * jt + 4 * q4;
+          const F4 bj = *(const F4*)&sb[j];
+          const float bi = sb[i];
+          uint32_t hi[2], lo[2];
+          float f[4], tri[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float e = __builtin_amdgcn_exp2f((float)(ci - sc[j + r]));
+            f[r] = j + r <= i ? p[r] * e * (DELTA ? 1.0f : bj[r]) : 0.0f;
+            if constexpr (DELTA) tri[r] = j + r < i ? -(bi * e * kk[r]) : 0.0f;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            hi[r] = upper2(f[2 * r], f[2 * r + 1]);
+            lo[r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
+          }
+          *(uint2*)&sp[0][i * kPR + j] = make_uint2(hi[0], hi[1]);
+          *(uint2*)&sp[1][i * kPR + j] = make_uint2(lo[0], lo[1]);
+          if constexpr (DELTA) *(F4*)&sa[i * kAR + j] = (F4){tri[0], tri[1], tri[2], tri[3]};
+        }
+      }
+      __syncthreads();
+      if constexpr (DELTA) {
+        // the four diagonal blocks of I + A inverted by substitution, a column each lane
+        if (wave == (t / kL) % WAVES) {
+          float x[16];
+          float* blk = &sa[(16 * q4) * kAR + 16 * q4];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y = i == m ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) y = fmaf(blk[i * kAR + j], x[j], y);
+            x[i] = y;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) blk[i * kAR + m] = x[i];
+        }
+      }
+      // ---- products with the state
+      F4 O[NV][4], R[DELTA ? NV : 1][4];
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          O[v][i] = (F4){0, 0, 0, 0};
+          if constexpr (DELTA) R[v][i] = (F4){0, 0, 0, 0};
+        }
+#pragma unroll
+      for (int c = 0; c < kKS; ++c) {
+        BF8 sp_[NV][DELTA ? 3 : 2];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = S[v][2 * c + (j >> 2)][j & 3];
+          split(f, sp_[v]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const BF8 qf = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            O[v][i] = mfma(qf, sp_[v][0], O[v][i]);
+            O[v][i] = mfma(qf, sp_[v][1], O[v][i]);
+          }
+          if constexpr (DELTA) {
+            const BF8 kf = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              R[v][i] = mfma(kf, sp_[v][0], R[v][i]);
+              R[v][i] = mfma(kf, sp_[v][1], R[v][i]);
+              R[v][i] = mfma(kf, sp_[v][2], R[v][i]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F4 e = *(const F4*)&se[16 * i + 4 * q4];
+        F4 bi = (F4){1, 1, 1, 1};
+        if constexpr (DELTA) bi = *(const F4*)&sb[16 * i + 4 * q4];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if constexpr (DELTA) {
+            const BF4 x = read_tr(&sv[(16 * i + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) R[v][i][r] = bi[r] * fmaf(-e[r], R[v][i][r], (float)x[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) O[v][i][r] *= e[r];
+        }
+      }
+      if constexpr (DELTA) {
+        __syncthreads();                     // the inverted blocks
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+          for (int x = 0; x < b; ++x) {
+            const F4 ab = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) R[v][b] = mfma1(ab[r], U[v][x][r], R[v][b]);
+          }
+          const F4 tb = *(const F4*)&sa[(16 * b + m) * kAR + 16 * b + 4 * q4];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            U[v][b] = (F4){0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) U[v][b] = mfma1(tb[r], R[v][b][r], U[v][b]);
+          }
+        }
+      }
+      // ---- outputs: P u on top
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        BF8 ub[NV][DELTA ? 2 : 1];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if constexpr (DELTA) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = U[v][2 * c + (j >> 2)][j & 3];
+            split(f, ub[v]);
+          } else {
+            const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
+            ub[v][0] = join(read_tr(x), read_tr(x + 16 * kVR));
+          }
+        }
+#pragma unroll
+        for (int i = 2 * c; i < 4; ++i) {
+          const uint16_t* x = &sp[0][(16 * i + m) * kPR + 32 * c + 4 * q4];
+          const uint16_t* y = &sp[1][(16 * i + m) * kPR + 32 * c + 4 * q4];
+          const BF8 ph = join(*(const BF4*)x, *(const BF4*)(x + 16)), pl = join(*(const BF4*)y, *(const BF4*)(y + 16));
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            O[v][i] = mfma(ph, ub[v][0], O[v][i]);
+            O[v][i] = mfma(pl, ub[v][0], O[v][i]);
+            if constexpr (DELTA) O[v][i] = mfma(ph, ub[v][1], O[v][i]);
+          }
+        }
+      }
+      // ---- the state update (below) still reads v; only then the outputs take its place
+      F4 W[2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) W[c][j] = *(const F4*)&sw[32 * c + 16 * j + 4 * q4];
+      BF8 wu[NV][2][3];
+      const float skip = a.skip ? a.skip[h] : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
+          const BF8 y = join(read_tr(x), read_tr(x + 16 * kVR));
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float vv = (float)y[j];
+            f[j] = W[c][j >> 2][j & 3] * (DELTA ? U[DELTA ? v : 0][2 * c + (j >> 2)][j & 3] : vv);
+            if (a.skip) O[v][2 * c + (j >> 2)][j & 3] = fmaf(skip, vv, O[v][2 * c + (j >> 2)][j & 3]);
+          }
+          split(f, wu[v][c]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const __bf16 y = (__bf16)O[v][i][r];
+            sv[(16 * i + 4 * q4 + r) * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+          }
+#pragma unroll
+      for (int t2 = 0; t2 < 2 * kKS; ++t2) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[v][t2][r] *= eall;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint16_t* x = &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * (t2 >> 1) + 8 * (m & 3) + 4 * (t2 & 1)];
+          const BF8 kt = join(read_tr(x), read_tr(x + 16 * kKR));
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) S[v][t2] = mfma(kt, wu[v][c][p], S[v][t2]);
+        }
+      }
+      __syncthreads();                       // outputs are in LDS, the chunk has been read
+#pragma unroll
+      for (int i = 0; i < kVP; ++i) {
+        const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+        if (r < n) {
+          const U4 y = *(const U4*)&sv[r * kVR + c];
+          uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
+          if (a.vec) {
+            if (v0 + c < a.dv) *(U4*)(o + c) = y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (v0 + c + j < a.dv) o[c + j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+          }
+        }
+      }
+    } else {
+      BF8 wu[NV][2][3];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
+          const BF8 y = join(read_tr(x), read_tr(x + 16 * kVR));
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = sw[32 * c + 16 * (j >> 2) + 4 * q4 + (j & 3)] * (float)y[j];
+          split(f, wu[v][c]);
+        }
+#pragma unroll
+      for (int t2 = 0; t2 < 2 * kKS; ++t2) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[v][t2][r] *= eall;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint16_t* x = &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * (t2 >> 1) + 8 * (m & 3) + 4 * (t2 & 1)];
+          const BF8 kt = join(read_tr(x), read_tr(x + 16 * kKR));
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) S[v][t2] = mfma(kt, wu[v][c][p], S[v][t2]);
+        }
+      }
+    }
+    t = next;
+  }
+
+  float* to = OUT ? (sg.last ? a.final + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
+                  : g.states + (int64_t)s * a.H * a.dv * DK;
+  if (to) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int col = v0 + vcol + 16 * v;
+      if (col < a.dv)
+#pragma unroll
+        for (int t = 0; t < 2 * kKS; ++t)
+          *(F4*)(to + (head + col) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1)) = S[v][t];
+    }
+  }
+  if (!OUT && tid == 0 && v0 == 0) g.total[(int64_t)s * a.H + h] = (float)total;
+}
+
+// States between segments: for each sequence, S = initial, then S = 2^total S + local
+// from segment to segment; segment s's place takes the state before it.
+__global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanSegs g, int blocks) {
+  const int seq = (int)blockIdx.x / blocks;
+  const int64_t per = (int64_t)a.dv * a.dk / 4, all = per * a.H;
+  const int64_t e = (int64_t)((int)blockIdx.x % blocks) * 256 + threadIdx.x;
+  if (e >= all) return;
+  const int h = (int)(e / per);
+  const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
+  const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
+  if (end <= start) return;
+  const int c0 = start / g.seg, c1 = (end - 1) / g.seg;
+  F4* st = (F4*)g.states;
+  F4 S = (F4){0, 0, 0, 0};
+  if (a.initial) S = ((const F4*)a.initial)[(int64_t)seq * all + e];
+  F4 L = (F4){0, 0, 0, 0};
+  if (c0 < c1) L = st[(int64_t)(c0 + seq) * all + e];
+  for (int c = c0; c < c1; ++c) {
+    const float d = __builtin_amdgcn_exp2f(g.total[(int64_t)(c + seq) * a.H + h]);
+    F4 next = (F4){0, 0, 0, 0};
+    if (c + 1 < c1) next = st[(int64_t)(c + 1 + seq) * all + e];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[r] = fmaf(d, S[r], L[r]);
+    st[(int64_t)(c + 1 + seq) * all + e] = S;
+    L = next;
+  }
+}
+
+template <int DK, int NV, int WAVES, bool DELTA>
+hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  const int vchunks = (a.dv + 16 * NV * WAVES - 1) / (16 * NV * WAVES);
+  const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
+  if constexpr (!DELTA) {
+    if (g.states) {
+      k_scan_chunk<DK, NV, WAVES, false, false><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+      const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
+      k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
+    }
+  }
+  k_scan_chunk<DK, NV, WAVES, DELTA, true><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+  return hipGetLastError();
+}
+
+template <int DK>
+hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  if (a.delta) return chunk<DK, 1, 4, true>(a, g, s);
+  return chunk<DK, 2, 2, false>(a, g, s);
+}
+
+}  // namespace
+
+hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.dk == 64 ? chunk_dk<64>(a, g, s) : a.dk == 128 ? chunk_dk<128>(a, g, s) : chunk_dk<256>(a, g, s);
+}
+
+}  // namespace qs

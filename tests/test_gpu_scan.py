@@ -253,3 +253,39 @@ def test_serving_run():
         got = torch.stack([s[i] for s in os_])
         check("delta", "fp32", [steps], dk, got, pool_qs.dequantize(pool)[now[i]][None], ref)
     pool_qs.close(), some_qs.close()
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("where,value", [("v", float("nan")), ("v", float("inf")), ("k", float("nan")),
+                                         ("decay", float("nan")), ("beta", float("inf")), ("q", float("nan"))])
+def test_scan_later_tokens_do_not_reach_earlier_ones(kind, decay, where, value):
+    """A value that is not finite at a token leaves every earlier output as it is, and every other sequence."""
+    lengths, bad = [150, 40], (70, 75)
+    q, k, v, d, b = inputs(kind, decay, lengths, 2, 2, 64, 48, "bf16")
+    args = dict(q=q, k=k, v=v, decay=d, beta=b)
+    qs = QState(StateConfig(kind=kind, decay_mode=decay, B=2, H=2, dk=64, dv=48))
+    clean, cfin = qs.scan(*(x.to(DEV) for x in (q, k, v, d, b)), offsets=offsets(lengths))
+    x = args[where].clone()
+    for t in bad:
+        x[t].view(-1)[3 if x[t].numel() > 3 else 0] = value
+    args[where] = x
+    out, fin = qs.scan(*(args[n].to(DEV) for n in ("q", "k", "v", "decay", "beta")), offsets=offsets(lengths))
+    torch.cuda.synchronize()
+    same = lambda a, c: torch.allclose(a.float(), c.float(), rtol=2 ** -7, atol=1e-3)
+    assert torch.isfinite(out[:bad[0]]).all() and same(out[:bad[0]], clean[:bad[0]])
+    assert torch.isfinite(out[150:]).all() and same(out[150:], clean[150:]) and torch.equal(fin[1], cfin[1])
+    assert not torch.isfinite(out[bad[0]:150]).all()
+    if where == "v":                                    # only that head's value row
+        ok = torch.ones(2, 48, dtype=torch.bool)
+        ok[0, 3] = False
+        assert torch.isfinite(out[:, ok]).all() and same(out[:, ok], clean[:, ok])
+    if where == "q":                                    # nothing of it stays
+        assert torch.equal(fin, cfin)
+    qs.close()
+
+
+@pytest.mark.parametrize("kind", ["additive", "delta"])
+def test_scan_long_and_many_heads(kind):
+    """Long enough to be cut into segments, over cells' and sequences' boundaries."""
+    run(kind, "head", [700, 1, 0, 1300, 64, 47], 4, 2, 64, 40, "bf16", initial=True, skip=True, mu=5.0)
+    run(kind, "head", [2048], 2, 1, 128, 64, "bf16", mu=6.0)
