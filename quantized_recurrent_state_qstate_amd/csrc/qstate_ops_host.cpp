@@ -291,7 +291,6 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   if ((int64_t)p.segs.count * a.H * ((a.dv + 31) / 32) > 0x7FFFFFFF ||
       (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > 0x7FFFFFFF)
     return op_fail(QS_EUNSUPPORTED, "%d tokens of %d sequences in one call", a.T, a.n);
-  if ((s = qs::op_check_device(h)) != QS_OK) return s;
   a.q = c->q;
   a.k = c->k;
   a.v = c->v;
@@ -309,9 +308,13 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   a.bs = c->beta_stride;
   a.os = c->out_stride;
   const int64_t v = 16 / es;
+  const int64_t far = int64_t(1) << 24;   // the kernels keep offsets within 64 rows in 32 bits
+  if (p.chunked && T > 1 && (c->q_stride > far || c->k_stride > far || c->v_stride > far))
+    return op_fail(QS_EUNSUPPORTED, "a stride of more than 2^24 elements");
   a.vec = aligned(c->q, 16) && aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->out, 16) && vw % v == 0 &&
           a.dv % v == 0 && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0 && c->v_stride % v == 0 &&
                                        c->out_stride % v == 0));
+  if ((s = qs::op_check_device(h)) != QS_OK) return s;
   hipError_t e = p.chunked ? qs::launch_scan_chunk(a, p.segs, reinterpret_cast<hipStream_t>(stream))
                            : qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));

@@ -58,8 +58,9 @@ __device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper ha
 }
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t round2(float a, float b) {
-  const __bf16 x = (__bf16)a, y = (__bf16)b;
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+  using F2 = float __attribute__((ext_vector_type(2)));
+  using B2 = __bf16 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(((F2){a, b}), B2));
 }
 template <int N>
 __device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
@@ -85,6 +86,25 @@ __device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
 
 __device__ __forceinline__ BF8 join(BF4 a, BF4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Inclusive sums over the wave's 64 lanes, by DPP moves of the two halves:
+// shifts within rows of 16, then the last lane of a row, of a half, on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ double wave_sums(double x) {
+  x += shifted<0x111, 0xF>(x);
+  x += shifted<0x112, 0xF>(x);
+  x += shifted<0x114, 0xF>(x);
+  x += shifted<0x118, 0xF>(x);
+  x += shifted<0x142, 0xA>(x);
+  x += shifted<0x143, 0xC>(x);
+  return x;
 }
 
 // Segment s of the packed tokens.  Segment s = (sequence i, cell c) with
@@ -121,29 +141,48 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
   return r;
 }
 
-// 16 bytes of a bf16 row: 8 elements from column c of `width`.
-__device__ __forceinline__ U4 load8(const void* p, int64_t row, int c, int width, bool vec) {
-  const uint16_t* x = (const uint16_t*)p + row;
-  if (vec) return c < width ? *(const U4*)(x + c) : (U4){0, 0, 0, 0};
-  uint32_t d[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = c + 2 * j < width ? x[c + 2 * j] : 0u, hi = c + 2 * j + 1 < width ? x[c + 2 * j + 1] : 0u;
-    d[j] = lo | (hi << 16);
+// 64 rows of a bf16 tensor from row t0's element `p` on, `n` of them real: 16-byte
+// pieces of `width` elements, zeros behind the last row.  VEC: buffer loads,
+// whose bound is the last real row's end (rows are at most 2^24 elements
+// apart, so offsets fit; a piece that begins in a row begins in front of the
+// bound, and pieces are 16-byte aligned within it).
+template <bool VEC>
+struct Tile {
+  const uint16_t* p;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int32_t stride, n, width;
+  __device__ __forceinline__ Tile(const void* base, int64_t at, int64_t row, int n_, int width_)
+      : p((const uint16_t*)base + at), stride((int32_t)row), n(n_), width(width_) {
+    if constexpr (VEC)
+      rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, n > 0 ? ((n - 1) * stride + width) * 2 : 0, 0x00027000);
   }
-  return (U4){d[0], d[1], d[2], d[3]};
-}
-
-__device__ __forceinline__ bool odd8(U4 u) {    // an infinity or NaN among 8 bf16 numbers
-  bool bad = false;
+  __device__ __forceinline__ U4 load(int r, int c) const {
+    if constexpr (VEC) {
+      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (r * stride + c) * 2, 0, 0));
+    } else {
+      uint32_t d[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    bad = bad || (u[j] & 0x7F80u) == 0x7F80u || (u[j] & 0x7F800000u) == 0x7F800000u;
-  return bad;
-}
+      for (int j = 0; j < 4; ++j) {
+        const int64_t e = (int64_t)r * stride + c + 2 * j;
+        const uint32_t lo = r < n && c + 2 * j < width ? p[e] : 0u, hi = r < n && c + 2 * j + 1 < width ? p[e + 1] : 0u;
+        d[j] = lo | (hi << 16);
+      }
+      return (U4){d[0], d[1], d[2], d[3]};
+    }
+  }
+};
 
-template <int DK, int NV, int WAVES, bool DELTA, bool OUT>
-__global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
+// The largest exponents (as 15-bit patterns without sign) of 8 bf16 numbers, by halves.
+using H2 = uint16_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ H2 largest(H2 x, U4 u) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x = __builtin_elementwise_max(x, __builtin_bit_cast(H2, u[j] & 0x7FFF7FFFu));
+  return x;
+}
+__device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
+
+template <int DK, int NV, int WAVES, bool DELTA, bool OUT, bool VEC>
+__global__ __launch_bounds__(64 * WAVES, DK <= 128 ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kT = 64 * WAVES;            // threads
   constexpr int kDV = 16 * NV * WAVES;      // value columns
   constexpr int kKS = DK / 32;              // steps of 32 channels
@@ -183,30 +222,23 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
       if (from && v < a.dv) S[n][t] = *(const F4*)(from + (head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
     }
   }
-  if (OUT) {
-    // the P tiles right of the diagonal that a step of 32 tokens reads stay zero
-    for (int i = tid; i < 2 * 16 * 16; i += kT) {
-      const int b = i >> 8, r = (i >> 4) & 15, c = i & 15;
-      sp[0][(32 * b + r) * kPR + 32 * b + 16 + c] = 0;
-      sp[1][(32 * b + r) * kPR + 32 * b + 16 + c] = 0;
-    }
-  }
-
   U4 nk[kKP], nq[OUT ? kKP : 1], nv[kVP];
   float nd = 1.0f, nb = 0.0f;
   auto fetch = [&](int t, int t1) {
+    const int rows = min(kL, t1 - t);
+    const Tile<VEC> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
+    const Tile<VEC> tq(OUT ? a.q : a.k, OUT ? (int64_t)t * a.qs + (int64_t)kh * DK : 0, a.qs, rows, DK);
+    const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
       const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-      const bool in = t + r < t1;
-      nk[i] = in ? load8(a.k, (int64_t)(t + r) * a.ks + (int64_t)kh * DK, c, DK, a.vec) : (U4){0, 0, 0, 0};
-      if constexpr (OUT)
-        nq[i] = in ? load8(a.q, (int64_t)(t + r) * a.qs + (int64_t)kh * DK, c, DK, a.vec) : (U4){0, 0, 0, 0};
+      nk[i] = tk.load(r, c);
+      if constexpr (OUT) nq[i] = tq.load(r, c);
     }
 #pragma unroll
     for (int i = 0; i < kVP; ++i) {
       const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      nv[i] = t + r < t1 ? load8(a.v, (int64_t)(t + r) * a.vs + head + v0, c, a.dv - v0, a.vec) : (U4){0, 0, 0, 0};
+      nv[i] = tv.load(r, c);
     }
     nd = 1.0f;
     nb = 0.0f;
@@ -215,23 +247,63 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
       nb = a.beta ? a.beta[(int64_t)(t + tid) * a.bs + h] : 1.0f;
     }
   };
-  // The token of a chunk (behind its first) whose k, v or gates are not
-  // finite begins a chunk of its own: a product with a zero of P or of the
-  // triangle would carry it to the tokens before it.
+  // The token of a chunk (behind its first) whose v, or in the delta rule k or
+  // gates, are not finite begins a chunk of its own: a product with a zero of P
+  // or of the triangle would carry it to the tokens before it.
   auto note_bad = [&](int n) {
-    int bad = kL;
+    H2 most = (H2){0, 0};
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < kKP; ++i) {
-      const int r = (i * kT + tid) / (DK / 8);
-      if (r > 0 && odd8(nk[i])) bad = min(bad, r);
+    for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
+    if constexpr (DELTA) {
+#pragma unroll
+      for (int i = 0; i < kKP; ++i) most = largest(most, nk[i]);
+      any = tid < kL && !(fabsf(nd) < INFINITY && fabsf(nb) < INFINITY);
     }
+    if (!any && !odd(most)) return;
+    int bad = any && tid > 0 ? tid : kL;
 #pragma unroll
     for (int i = 0; i < kVP; ++i) {
       const int r = (i * kT + tid) / (kDV / 8);
-      if (r > 0 && odd8(nv[i])) bad = min(bad, r);
+      if (r > 0 && odd(largest((H2){0, 0}, nv[i]))) bad = min(bad, r);
     }
-    if (tid > 0 && tid < kL && !(fabsf(nd) < INFINITY && fabsf(nb) < INFINITY)) bad = min(bad, tid);
+    if constexpr (DELTA) {
+#pragma unroll
+      for (int i = 0; i < kKP; ++i) {
+        const int r = (i * kT + tid) / (DK / 8);
+        if (r > 0 && odd(largest((H2){0, 0}, nk[i]))) bad = min(bad, r);
+      }
+    }
     if (bad < n) atomicMin(&sbad, bad);
+  };
+
+  // S = 2^{c of the last token} S + sum_j k_j (w_j u_j)^T, four tiles at a time
+  auto update = [&](const BF8 (&wu)[NV][2][3], float eall) {
+#pragma unroll
+    for (int t4 = 0; t4 < 2 * kKS; t4 += 4) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int t = t4; t < t4 + 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[v][t][r] *= eall;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        BF8 kt[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint16_t* x =
+              &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * ((t4 + t) >> 1) + 8 * (m & 3) + 4 * (t & 1)];
+          kt[t] = join(read_tr(x), read_tr(x + 16 * kKR));
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[v][t4 + t] = mfma(kt[t], wu[v][c][p], S[v][t4 + t]);
+      }
+    }
   };
 
   if (tid == 0) sbad = kL;
@@ -241,14 +313,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
   for (int t = sg.t0; t < sg.t1;) {
     int n = min(kL, sg.t1 - t);
     // ---- this chunk into LDS; gates
-    note_bad(n);
-    __syncthreads();                         // sbad is known; the chunk before has been read
-    const int cutoff = sbad;
-    __syncthreads();
-    if (cutoff < n) {
-      n = cutoff;
+    if constexpr (OUT) note_bad(n);
+    __syncthreads();                         // the chunk before has been read; sbad is known
+    const bool cutoff = OUT && sbad < n;
+    if (cutoff) {
+      n = sbad;
       fetch(t, t + n);
-      if (tid == 0) sbad = kL;
     }
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
@@ -262,12 +332,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
       *(U4*)&sv[r * kVR + c] = nv[i];
     }
     if (wave == 0) {
-      double c = nd == 0.0f ? -10000.0 : (double)log2f(nd);
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double x = __shfl_up(c, o);
-        if (lane >= o) c += x;
-      }
+      const double c = wave_sums(nd == 0.0f ? -10000.0 : (double)log2f(nd));
       const double all = __shfl(c, 63);
       sc[lane] = c;
       sb[lane] = nb;
@@ -275,6 +340,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
       sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * (DELTA ? 1.0f : nb);
     }
     __syncthreads();
+    if (cutoff && tid == 0) sbad = kL;       // read by all, and next written behind the chunk's other barriers
     const int next = t + n;
     if (next < sg.t1) fetch(next, sg.t1);
     const double call = sc[kL - 1];
@@ -289,33 +355,51 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
         const int it = WAVES == 4 ? wave : (x ? 3 - wave : wave);
         const int i = 16 * it + m;
         const double ci = sc[i];
-        for (int jt = 0; jt <= it; ++jt) {
-          F4 p = (F4){0, 0, 0, 0}, kk = (F4){0, 0, 0, 0};
+        // two tiles at a time, to the end of the step of 32 that the products below
+        // read: right of the diagonal they become zeros
+        for (int jp = 0; jp <= it; jp += 2) {
+          F4 p[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}}, kk[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}};
 #pragma unroll
           for (int c = 0; c < kKS; ++c) {
-            const BF8 kj = *(const BF8*)&sk[(16 * jt + m) * kKR + 32 * c + 8 * q4];
-            p = mfma(kj, *(const BF8*)&sq[i * kKR + 32 * c + 8 * q4], p);
-            if constexpr (DELTA) kk = mfma(kj, *(const BF8*)&sk[i * kKR + 32 * c + 8 * q4], kk);
+            const BF8 qi = *(const BF8*)&sq[i * kKR + 32 * c + 8 * q4];
+            BF8 ki{};
+            if constexpr (DELTA) ki = *(const BF8*)&sk[i * kKR + 32 * c + 8 * q4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const BF8 kj = *(const BF8*)&sk[(16 * (jp + y) + m) * kKR + 32 * c + 8 * q4];
+              p[y] = mfma(kj, qi, p[y]);
+              if constexpr (DELTA) kk[y] = mfma(kj, ki, kk[y]);
+            }
           }
-          const int j = 16 * jt + 4 * q4;
-          const F4 bj = *(const F4*)&sb[j];
           const float bi = sb[i];
-          uint32_t hi[2], lo[2];
-          float f[4], tri[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = __builtin_amdgcn_exp2f((float)(ci - sc[j + r]));
-            f[r] = j + r <= i ? p[r] * e * (DELTA ? 1.0f : bj[r]) : 0.0f;
-            if constexpr (DELTA) tri[r] = j + r < i ? -(bi * e * kk[r]) : 0.0f;
-          }
+          for (int y = 0; y < 2; ++y) {
+            const int j = 16 * (jp + y) + 4 * q4;
+            const F4 bj = *(const F4*)&sb[j];
+            double cj[4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            hi[r] = upper2(f[2 * r], f[2 * r + 1]);
-            lo[r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
+            for (int r = 0; r < 4; ++r) cj[r] = sc[j + r];
+            uint32_t hi[2], lo[2];
+            float f[4], tri[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float e = __builtin_amdgcn_exp2f((float)(ci - cj[r]));
+              const float w = p[y][r] * e * (DELTA ? 1.0f : bj[r]);
+              f[r] = j + r <= i ? w : 0.0f;
+              if constexpr (DELTA) {
+                const float z = -(bi * e * kk[y][r]);
+                tri[r] = j + r < i ? z : 0.0f;
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              hi[r] = upper2(f[2 * r], f[2 * r + 1]);
+              lo[r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
+            }
+            *(uint2*)&sp[0][i * kPR + j] = make_uint2(hi[0], hi[1]);
+            *(uint2*)&sp[1][i * kPR + j] = make_uint2(lo[0], lo[1]);
+            if constexpr (DELTA) *(F4*)&sa[i * kAR + j] = (F4){tri[0], tri[1], tri[2], tri[3]};
           }
-          *(uint2*)&sp[0][i * kPR + j] = make_uint2(hi[0], hi[1]);
-          *(uint2*)&sp[1][i * kPR + j] = make_uint2(lo[0], lo[1]);
-          if constexpr (DELTA) *(F4*)&sa[i * kAR + j] = (F4){tri[0], tri[1], tri[2], tri[3]};
         }
       }
       __syncthreads();
@@ -354,24 +438,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
           for (int j = 0; j < 8; ++j) f[j] = S[v][2 * c + (j >> 2)][j & 3];
           split(f, sp_[v]);
         }
+        BF8 qf[4], kf[DELTA ? 4 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const BF8 qf = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            O[v][i] = mfma(qf, sp_[v][0], O[v][i]);
-            O[v][i] = mfma(qf, sp_[v][1], O[v][i]);
-          }
-          if constexpr (DELTA) {
-            const BF8 kf = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              R[v][i] = mfma(kf, sp_[v][0], R[v][i]);
-              R[v][i] = mfma(kf, sp_[v][1], R[v][i]);
-              R[v][i] = mfma(kf, sp_[v][2], R[v][i]);
-            }
-          }
+          qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
+          if constexpr (DELTA) kf[i] = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
         }
+        // products on one accumulator are kept apart: each takes several issue slots
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (x < 2) O[v][i] = mfma(qf[i], sp_[v][x < 2 ? x : 0], O[v][i]);
+              if constexpr (DELTA) R[v][i] = mfma(kf[i], sp_[v][DELTA ? x : 0], R[v][i]);
+            }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -393,14 +475,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
         __syncthreads();                     // the inverted blocks
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-#pragma unroll
-          for (int x = 0; x < b; ++x) {
-            const F4 ab = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) R[v][b] = mfma1(ab[r], U[v][x][r], R[v][b]);
-          }
           const F4 tb = *(const F4*)&sa[(16 * b + m) * kAR + 16 * b + 4 * q4];
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
@@ -408,6 +482,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
 #pragma unroll
             for (int r = 0; r < 4; ++r) U[v][b] = mfma1(tb[r], R[v][b][r], U[v][b]);
           }
+          F4 ab[3];
+#pragma unroll
+          for (int x = b + 1; x < 4; ++x) ab[x - 1] = *(const F4*)&sa[(16 * x + m) * kAR + 16 * b + 4 * q4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int x = b + 1; x < 4; ++x)
+#pragma unroll
+              for (int v = 0; v < NV; ++v) R[v][x] = mfma1(ab[x - 1][r], U[v][b][r], R[v][x]);
         }
       }
       // ---- outputs: P u on top
@@ -426,18 +509,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
             ub[v][0] = join(read_tr(x), read_tr(x + 16 * kVR));
           }
         }
+        BF8 ph[4], pl[4];
 #pragma unroll
         for (int i = 2 * c; i < 4; ++i) {
           const uint16_t* x = &sp[0][(16 * i + m) * kPR + 32 * c + 4 * q4];
           const uint16_t* y = &sp[1][(16 * i + m) * kPR + 32 * c + 4 * q4];
-          const BF8 ph = join(*(const BF4*)x, *(const BF4*)(x + 16)), pl = join(*(const BF4*)y, *(const BF4*)(y + 16));
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            O[v][i] = mfma(ph, ub[v][0], O[v][i]);
-            O[v][i] = mfma(pl, ub[v][0], O[v][i]);
-            if constexpr (DELTA) O[v][i] = mfma(ph, ub[v][1], O[v][i]);
-          }
+          ph[i] = join(*(const BF4*)x, *(const BF4*)(x + 16));
+          pl[i] = join(*(const BF4*)y, *(const BF4*)(y + 16));
         }
+#pragma unroll
+        for (int x = 0; x < (DELTA ? 3 : 2); ++x)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 2 * c; i < 4; ++i)
+              O[v][i] = mfma(x == 1 ? pl[i] : ph[i], ub[v][DELTA && x == 2 ? 1 : 0], O[v][i]);
       }
       // ---- the state update (below) still reads v; only then the outputs take its place
       F4 W[2][2];
@@ -471,22 +557,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
             const __bf16 y = (__bf16)O[v][i][r];
             sv[(16 * i + 4 * q4 + r) * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
           }
-#pragma unroll
-      for (int t2 = 0; t2 < 2 * kKS; ++t2) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[v][t2][r] *= eall;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint16_t* x = &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * (t2 >> 1) + 8 * (m & 3) + 4 * (t2 & 1)];
-          const BF8 kt = join(read_tr(x), read_tr(x + 16 * kKR));
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int p = 0; p < 3; ++p) S[v][t2] = mfma(kt, wu[v][c][p], S[v][t2]);
-        }
-      }
+      update(wu, eall);
       __syncthreads();                       // outputs are in LDS, the chunk has been read
 #pragma unroll
       for (int i = 0; i < kVP; ++i) {
@@ -494,7 +565,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
         if (r < n) {
           const U4 y = *(const U4*)&sv[r * kVR + c];
           uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
-          if (a.vec) {
+          if constexpr (VEC) {
             if (v0 + c < a.dv) *(U4*)(o + c) = y;
           } else {
 #pragma unroll
@@ -516,22 +587,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scan_chunk(const ScanArgs a, con
           for (int j = 0; j < 8; ++j) f[j] = sw[32 * c + 16 * (j >> 2) + 4 * q4 + (j & 3)] * (float)y[j];
           split(f, wu[v][c]);
         }
-#pragma unroll
-      for (int t2 = 0; t2 < 2 * kKS; ++t2) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[v][t2][r] *= eall;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint16_t* x = &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * (t2 >> 1) + 8 * (m & 3) + 4 * (t2 & 1)];
-          const BF8 kt = join(read_tr(x), read_tr(x + 16 * kKR));
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int p = 0; p < 3; ++p) S[v][t2] = mfma(kt, wu[v][c][p], S[v][t2]);
-        }
-      }
+      update(wu, eall);
     }
     t = next;
   }
@@ -579,25 +635,25 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
   }
 }
 
-template <int DK, int NV, int WAVES, bool DELTA>
+template <int DK, int NV, int WAVES, bool DELTA, bool VEC>
 hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int vchunks = (a.dv + 16 * NV * WAVES - 1) / (16 * NV * WAVES);
   const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
   if constexpr (!DELTA) {
     if (g.states) {
-      k_scan_chunk<DK, NV, WAVES, false, false><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+      k_scan_chunk<DK, NV, WAVES, false, false, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
       const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
       k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
     }
   }
-  k_scan_chunk<DK, NV, WAVES, DELTA, true><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+  k_scan_chunk<DK, NV, WAVES, DELTA, true, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
   return hipGetLastError();
 }
 
 template <int DK>
 hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  if (a.delta) return chunk<DK, 1, 4, true>(a, g, s);
-  return chunk<DK, 2, 2, false>(a, g, s);
+  if (a.delta) return a.vec ? chunk<DK, 1, 4, true, true>(a, g, s) : chunk<DK, 1, 4, true, false>(a, g, s);
+  return a.vec ? chunk<DK, 1, 4, false, true>(a, g, s) : chunk<DK, 1, 4, false, false>(a, g, s);
 }
 
 }  // namespace
