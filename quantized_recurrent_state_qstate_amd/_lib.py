@@ -52,6 +52,9 @@ class Sizes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("codes", "scales", "hp", "lrb_W", "lrb_U", "lrb_n")]
 
 
+TENSORS = ("codes", "scales", "hp", "lrb_W", "lrb_U", "lrb_n")
+
+
 class Tensors(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("hp", ctypes.c_void_p),
                 ("lrb_W", ctypes.c_void_p), ("lrb_U", ctypes.c_void_p), ("lrb_n", ctypes.c_void_p)]

@@ -95,12 +95,18 @@ def _state_dtypes(cfg: "StateConfig") -> dict:
     return {"codes": "uint8", "scales": sd, "hp": "uint8", "lrb_W": ld, "lrb_U": ld, "lrb_n": "int32"}
 
 
+_ITEM = {"uint8": 1, "bfloat16": 2, "float32": 4, "int32": 4}
+
+
 def check_tensor(name: str, t, dtype, numel: int, device, at_least: bool = False) -> None:
     """Host-side argument check before a pointer crosses the C ABI: the kernels
     read and write exactly the planned extents, so a tensor of the wrong dtype,
     size, memory layout or device would make them read or write out of bounds
     or get wrong results.  Raises ValueError (checks in that order)."""
     import torch
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (t.numel() == numel or (at_least and t.numel() > numel))):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -120,9 +126,7 @@ def check_state(cfg: "StateConfig", sizes: dict, st: dict, device) -> None:
         nbytes = sizes[n]
         if nbytes == 0:
             continue
-        dtype = getattr(torch, dt)
-        item = torch.empty((), dtype=dtype).element_size()
-        check_tensor(f"state[{n!r}]", st.get(n), dtype, nbytes // item, device, at_least=True)
+        check_tensor(f"state[{n!r}]", st.get(n), getattr(torch, dt), nbytes // _ITEM[dt], device, at_least=True)
 
 
 def check_inputs(cfg: "StateConfig", n: int, device, q, k, v, decay, beta, out) -> None:
@@ -145,6 +149,9 @@ def check_rows(name: str, t, dtype, shape, device) -> int:
     """A tensor of `shape` whose rows (all dimensions but the first) are
     contiguous, at any stride between them; returns that stride in elements."""
     import torch
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.stride(0) if shape[0] > 1 else t.numel()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -172,6 +179,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def raw_stream(stream, device) -> int:
+    """The hipStream_t of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class QState:
@@ -314,42 +329,43 @@ class QState:
                 raise ValueError("offsets must be an int32 tensor [n+1]")
             n = offsets.numel() - 1
             check_tensor("offsets", offsets, torch.int32, n + 1, dev)
-        a = _lib.Scan()
-        a.q_stride = check_rows("q", q, ind, (T, G, c.dk), dev)
-        a.k_stride = check_rows("k", k, ind, (T, G, c.dk), dev)
-        a.v_stride = check_rows("v", v, ind, (T, c.H, c.dv), dev)
-        a.decay_stride = check_rows("decay", decay, torch.float32,
-                                    (T, c.H, c.dk) if c.decay_mode == "key" else (T, c.H), dev)
-        if beta is not None:
-            a.beta_stride = check_rows("beta", beta, torch.float32, (T, c.H), dev)
-            a.beta = beta.data_ptr()
+        H, dk, dv, f32 = c.H, c.dk, c.dv, torch.float32
+        qs = check_rows("q", q, ind, (T, G, dk), dev)
+        ks = check_rows("k", k, ind, (T, G, dk), dev)
+        vs = check_rows("v", v, ind, (T, H, dv), dev)
+        ds = check_rows("decay", decay, f32, (T, H, dk) if c.decay_mode == "key" else (T, H), dev)
+        bs = 0 if beta is None else check_rows("beta", beta, f32, (T, H), dev)
         if skip is not None:
-            check_tensor("skip", skip, torch.float32, c.H, dev)
-            a.skip = skip.data_ptr()
-        state = n * c.H * c.dv * c.dk
+            check_tensor("skip", skip, f32, H, dev)
         if initial is not None:
-            check_tensor("initial", initial, torch.float32, state, dev)
-            a.initial = initial.data_ptr()
+            check_tensor("initial", initial, f32, n * H * dv * dk, dev)
         if out is None:
-            out = _empty((T, c.H, c.dv), ind, dev, stream)
-        a.out_stride = check_rows("out", out, ind, (T, c.H, c.dv), dev)
-        if final is None:
-            final = _empty((n, c.H, c.dv, c.dk), torch.float32, dev, stream)
+            out = _empty((T, H, dv), ind, dev, stream)
+            os = H * dv
         else:
-            check_tensor("final", final, torch.float32, state, dev)
-        a.q, a.k, a.v, a.decay = q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr()
-        a.out, a.final, a.offsets = out.data_ptr(), final.data_ptr(), _ptr(offsets)
-        a.tokens, a.n, a.k_heads = T, n, G
+            os = check_rows("out", out, ind, (T, H, dv), dev)
+        if final is None:
+            final = _empty((n, H, dv, dk), f32, dev, stream)
+        else:
+            check_tensor("final", final, f32, n * H * dv * dk, dev)
+        a = _lib.Scan(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(beta), _ptr(skip),
+                      _ptr(initial), final.data_ptr(), out.data_ptr(), _ptr(offsets), qs, ks, vs, ds, bs, os, T, n, G)
         L = _lib.lib()
         need = ctypes.c_uint64()
         _lib.check(L.qstate_scan_workspace(self._h, ctypes.byref(a), ctypes.byref(need)), "qstate_scan_workspace")
         # the call's own: a captured call keeps it in its graph's memory
         ws = _empty((need.value,), torch.uint8, dev, stream) if need.value else None
-        _lib.check(L.qstate_scan(self._h, ctypes.byref(a), _ptr(ws), need.value, self._stream(stream)), "qstate_scan")
+        _lib.check(L.qstate_scan(self._h, ctypes.byref(a), _ptr(ws), need.value, raw_stream(stream, dev)),
+                   "qstate_scan")
         return out, final
 
-    def _slot_bytes(self, st: dict, name: str) -> int:
-        return self.sizes[name] // self.cfg.B if self.cfg.B else 0
+    def _checked(self, st: dict, slots: int) -> _lib.Tensors:
+        """The buffers of a state of `slots` slots, checked, as the C ABI takes them."""
+        B = self.cfg.B
+        check_state(self.cfg, self.sizes if slots == B else {n: z // B * slots if B else 0 for n, z in self.sizes.items()},
+                    st, self.device)
+        ptrs = [st.get(n) for n in _lib.TENSORS]
+        return _lib.Tensors(*[x.data_ptr() if x is not None and x.numel() > 0 else None for x in ptrs])
 
     def _extra(self, extra, source_extra, src_slots: int):
         """Per-slot buffers that go along: tensors [slots, ...], contiguous, on this device."""
@@ -394,12 +410,12 @@ class QState:
             if extra and source_extra is None and source is not pool:
                 raise ValueError("extra buffers of another pool need source_extra")
             m = int(source_slots)
-            check_state(self.cfg, {k: self._slot_bytes(source, k) * m for k in self.sizes}, source, self.device)
-        check_state(self.cfg, self.sizes, pool, self.device)
-        bufs, ne = self._extra(extra, source_extra, m)
-        d, s = self._tensors(pool), self._tensors(source)
+        d = self._checked(pool, self.cfg.B)
+        s = d if source is pool else self._checked(source, m)
+        bufs, ne = self._extra(extra, source_extra, m) if extra or source_extra else (None, 0)
         _lib.check(_lib.lib().qstate_copy_slots(self._h, ctypes.byref(d), ctypes.byref(s), m, n, _ptr(src_slot),
-                                                _ptr(dst_slot), bufs, ne, self._stream(stream)), "qstate_copy_slots")
+                                                _ptr(dst_slot), bufs, ne, raw_stream(stream, self.device)),
+                   "qstate_copy_slots")
 
     def compact_slots(self, pool: dict, live, *, extra=(), where=None, stream=None):
         """Move the live slots of `pool` (live: uint8 or bool [B], device) to
@@ -415,9 +431,8 @@ class QState:
         if where is None:
             where = _empty((c.B,), torch.int32, self.device, stream)
         check_tensor("where", where, torch.int32, c.B, self.device)
-        check_state(c, self.sizes, pool, self.device)
-        bufs, ne = self._extra(extra, None, c.B)
-        t = self._tensors(pool)
+        t = self._checked(pool, c.B)
+        bufs, ne = self._extra(extra, None, c.B) if extra else (None, 0)
         _lib.check(_lib.lib().qstate_compact_slots(self._h, ctypes.byref(t), _ptr(live), _ptr(where), bufs, ne,
-                                                   self._stream(stream)), "qstate_compact_slots")
+                                                   raw_stream(stream, self.device)), "qstate_compact_slots")
         return where

@@ -182,7 +182,7 @@ __device__ __forceinline__ H2 largest(H2 x, U4 u) {
 __device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
 
 template <int DK, int NV, int WAVES, bool DELTA, bool OUT, bool VEC>
-__global__ __launch_bounds__(64 * WAVES, DK <= 128 ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
+__global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kT = 64 * WAVES;            // threads
   constexpr int kDV = 16 * NV * WAVES;      // value columns
   constexpr int kKS = DK / 32;              // steps of 32 channels

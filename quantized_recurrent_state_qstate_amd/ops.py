@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .api import _empty, _ptr, check_rows, check_tensor
+from .api import _empty, _ptr, check_rows, check_tensor, raw_stream
 
 
 def _device(name: str, x):
@@ -25,15 +25,13 @@ def _call(fn, name: str, args, device, stream) -> None:
     import torch
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors on {device}, expected a GPU")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+    if stream is not None and stream.device != device:
         raise ValueError(f"stream on {stream.device}, expected {device}")
     if device.index == torch.cuda.current_device():
-        _lib.check(fn(ctypes.byref(args), stream.cuda_stream), name)
+        _lib.check(fn(ctypes.byref(args), raw_stream(stream, device)), name)
     else:
         with torch.cuda.device(device):
-            _lib.check(fn(ctypes.byref(args), stream.cuda_stream), name)
+            _lib.check(fn(ctypes.byref(args), raw_stream(stream, device)), name)
 
 
 def _conv(x, weight, bias, window, slot, n, silu, out, stream):
@@ -42,27 +40,25 @@ def _conv(x, weight, bias, window, slot, n, silu, out, stream):
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [tokens, C] and weight [W, C]")
     (T, C), W = x.shape, weight.shape[0]
-    a = _lib.Conv()
-    a.x_stride = check_rows("x", x, x.dtype, (T, C), dev)
+    dtype, slots = x.dtype, 0
+    xs = check_rows("x", x, dtype, (T, C), dev)
     check_tensor("weight", weight, torch.float32, W * C, dev)
     if bias is not None:
         check_tensor("bias", bias, torch.float32, C, dev)
-        a.bias = bias.data_ptr()
     if window is not None:
         if not isinstance(window, torch.Tensor) or window.dim() != 3:
             raise ValueError("window must be [slots, W-1, C]")
-        a.slots = window.shape[0]
-        check_tensor("window", window, x.dtype, a.slots * (W - 1) * C, dev)
-        a.window = window.data_ptr()
+        slots = window.shape[0]
+        check_tensor("window", window, dtype, slots * (W - 1) * C, dev)
     if slot is not None:
         check_tensor("slot", slot, torch.int32, n, dev)
-        a.slot = slot.data_ptr()
     if out is None:
-        out = _empty((T, C), x.dtype, dev, stream)
-    a.out_stride = check_rows("out", out, x.dtype, (T, C), dev)
-    a.x, a.out, a.weight = x.data_ptr(), out.data_ptr(), weight.data_ptr()
-    a.dtype = _lib.DTYPE["bf16" if x.dtype == torch.bfloat16 else "fp32"]
-    a.tokens, a.channels, a.width, a.n, a.silu = T, C, W, n, int(bool(silu))
+        out = _empty((T, C), dtype, dev, stream)
+        os = C
+    else:
+        os = check_rows("out", out, dtype, (T, C), dev)
+    a = _lib.Conv(x.data_ptr(), out.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(window), _ptr(slot), None, xs, os,
+                  _lib.DTYPE["bf16" if dtype is torch.bfloat16 else "fp32"], T, C, W, n, slots, 1 if silu else 0)
     return a, out, dev
 
 
@@ -116,38 +112,40 @@ def qk_norm_rotate(q, k=None, *, norm="l2", q_weight=None, k_weight=None, eps=1e
     dev = _device("q", q)
     if q.dim() != 3 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 3)):
         raise ValueError("q and k must be [T, heads, dim]")
-    T, hq, d = q.shape
-    a = _lib.Qk()
-    a.q_stride = check_rows("q", q, q.dtype, (T, hq, d), dev)
+    (T, hq, d), dtype = q.shape, q.dtype
+    hk = kp = ko = rot = 0
+    ks = kos = hq * d
+    qs = check_rows("q", q, dtype, (T, hq, d), dev)
     if q_out is None:
-        q_out = _empty((T, hq, d), q.dtype, dev, stream)
-    a.q_out_stride = check_rows("q_out", q_out, q.dtype, (T, hq, d), dev)
-    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+        q_out = _empty((T, hq, d), dtype, dev, stream)
+        qos = hq * d
+    else:
+        qos = check_rows("q_out", q_out, dtype, (T, hq, d), dev)
     if k is not None:
         hk = k.shape[1]
-        a.k_stride = check_rows("k", k, q.dtype, (T, hk, d), dev)
+        ks = check_rows("k", k, dtype, (T, hk, d), dev)
         if k_out is None:
-            k_out = _empty((T, hk, d), q.dtype, dev, stream)
-        a.k_out_stride = check_rows("k_out", k_out, q.dtype, (T, hk, d), dev)
-        a.k, a.k_out, a.k_heads = k.data_ptr(), k_out.data_ptr(), hk
+            k_out = _empty((T, hk, d), dtype, dev, stream)
+            kos = hk * d
+        else:
+            kos = check_rows("k_out", k_out, dtype, (T, hk, d), dev)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     if q_weight is not None:
         check_tensor("q_weight", q_weight, torch.float32, d, dev)
-        a.q_weight = q_weight.data_ptr()
     if k_weight is not None:
         check_tensor("k_weight", k_weight, torch.float32, d, dev)
-        a.k_weight = k_weight.data_ptr()
     if (frequency is None) != (position is None):
         raise ValueError("position and frequency go together")
     if frequency is not None:
         check_tensor("position", position, torch.int32, T, dev)
         check_tensor("frequency", frequency, torch.float64, frequency.numel(), dev)
-        a.position, a.frequency, a.rot = _ptr(position), _ptr(frequency), 2 * frequency.numel()
+        rot = 2 * frequency.numel()
     if norm not in _lib.NORM:
         raise ValueError(f"norm {norm!r} (l2, rms or none)")
-    a.dtype = _lib.DTYPE["bf16" if q.dtype == torch.bfloat16 else "fp32"]
-    a.tokens, a.q_heads, a.dim, a.norm = T, hq, d, _lib.NORM[norm]
-    a.interleaved, a.eps, a.q_scale = int(bool(interleaved)), eps, q_scale
+    a = _lib.Qk(q.data_ptr(), kp, q_out.data_ptr(), ko, _ptr(q_weight), _ptr(k_weight), _ptr(position),
+                _ptr(frequency), qs, ks, qos, kos, _lib.DTYPE["bf16" if dtype is torch.bfloat16 else "fp32"], T, hq,
+                hk, d, rot, _lib.NORM[norm], 1 if interleaved else 0, eps, q_scale)
     _call(_lib.lib().qstate_qk_norm_rotate, "qstate_qk_norm_rotate", a, dev, stream)
     return q_out, k_out
