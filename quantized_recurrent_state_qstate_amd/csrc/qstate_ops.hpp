@@ -94,13 +94,16 @@ struct ScanArgs {
 };
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
-// Segments of the chunked scan: cells of `seg` tokens of the packed axis,
-// cut again where sequences begin; `count` bounds their number.
+// Segments of the chunked scans: cells of `seg` tokens of the packed axis,
+// cut again where sequences begin; `count` bounds their number.  Delta rule:
+// seg is a chunk's 64 tokens, states its prepared matrices.
 struct ScanSegs {
   int32_t seg, count;
-  float* states;           // [count][H][dv][dk], null: no sequence is cut
+  float* states;           // [count][H][dv][dk], null: no sequence is cut; delta rule: [count][H] kScanPrepBytes
   float* total;            // [count][H] log2 of a segment's whole decay
 };
+constexpr int kScanPrepBytes = 1024 + 10 * 1024 + 12 * 1024;
+hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 
 }  // namespace qs

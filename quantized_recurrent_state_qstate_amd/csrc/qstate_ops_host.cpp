@@ -225,7 +225,13 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   p.chunked = a.bf16 && !a.key && a.T >= 64;
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
-  if (!p.chunked || a.delta) return p;
+  if (!p.chunked) return p;
+  if (a.delta) {
+    p.segs.seg = 64;
+    p.segs.count = (a.T + 63) / 64 + a.n;
+    p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)qs::kScanPrepBytes;
+    return p;
+  }
   const int64_t work = (int64_t)a.T * a.H * ((a.dv + 63) / 64);
   const int64_t seg = std::max<int64_t>(256, (work / 512 + 63) / 64 * 64);
   if (seg >= a.T) return p;
@@ -315,7 +321,7 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
           a.dv % v == 0 && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0 && c->v_stride % v == 0 &&
                                        c->out_stride % v == 0));
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
-  hipError_t e = p.chunked ? qs::launch_scan_chunk(a, p.segs, reinterpret_cast<hipStream_t>(stream))
+  hipError_t e = p.chunked ? (a.delta ? qs::launch_scan_delta : qs::launch_scan_chunk)(a, p.segs, reinterpret_cast<hipStream_t>(stream))
                            : qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));
   return op_ok();

@@ -1,201 +1,48 @@
-// Scan of packed bf16 prompts with one decay a head, 64 tokens at a time on
-// the matrix cores.
+// Scan of packed bf16 prompts, additive with one decay a head, 64 tokens at a
+// time on the matrix cores.
 //
-// With c_i the sum of log2 decays from a chunk's first token to token i and
-// S the state before the chunk,
+// With c_i the sum of log2 decays from a chunk's first token to token i, u = beta v
+// and S the state before the chunk,
 //   S_i = 2^{c_i} S + sum_{j<=i} 2^{c_i - c_j} u_j k_j^T,
-//   o_i = 2^{c_i} S q_i + sum_{j<=i} P_ij u_j,   P_ij = 2^{c_i - c_j} k_j.q_i,
-// and the state after the chunk is the last S_i.  Additive: u = beta v.  Delta
-// rule: u_i = beta_i (v_i - 2^{c_i} S k_i - sum_{j<i} 2^{c_i - c_j} (k_j.k_i) u_j),
-// a unit lower triangular system in the chunk's 64 rows, solved in fp32 by
-// blocks of 16: the diagonal blocks are inverted by substitution, the rest is
-// fp32 matrix instructions.
+//   o_i = 2^{c_i} S q_i + sum_{j<=i} P_ij v_j,   P_ij = 2^{c_i - c_j} beta_j k_j.q_i,
+// and the state after the chunk is the last S_i.
 //
 // Precision: q, k and v are bf16, so a product with one of them is exact when
-// the other operand is cut into bf16 pieces: three pieces (24 bits) of w u in
-// the state's update and of S in the delta rule's S k, two (16 bits) of S and
-// of P in the outputs, which are rounded to bf16 at the end.  All sums are fp32.
-// c is summed in fp64: differences of long sums of logs would lose the decays
-// between neighbours; a decay of zero counts as 2^-10000.
+// the other operand is cut into bf16 pieces: three pieces (24 bits) of w v in
+// the state's update, two (16 bits) of S and of P in the outputs, which are
+// rounded to bf16 at the end.  All sums are fp32.  c is summed in fp64:
+// differences of long sums of logs would lose the decays between neighbours;
+// a decay of zero counts as 2^-10000.
 //
 // A workgroup holds 16 NV WAVES value columns of one (segment, head): each wave
 // keeps the state of its columns in accumulators [dk][v], which are the second
-// operand of S q and S k as they are (the tiles' rows are dealt so that a lane
-// holds 8 channels in a row); k, q, v and P go through LDS.
+// operand of S q as they are (the tiles' rows are dealt so that a lane holds 8
+// channels in a row); k, q, v and P go through LDS.
 //
-// Segments: additive sequences may be cut at multiples of `seg` tokens.  Then
-// three launches: the state each segment adds by itself, the states between
+// Segments: sequences may be cut at multiples of `seg` tokens.  Then three
+// launches: the state each segment adds by itself, the states between
 // segments, and the outputs; so that few long sequences fill the device.
 #include <hip/hip_runtime.h>
 
-#include "qstate_ops.hpp"
+#include "qstate_scan_tiles.hpp"
 
 namespace qs {
 namespace {
 
-using BF8 = __bf16 __attribute__((ext_vector_type(8)));
-using BF4 = __bf16 __attribute__((ext_vector_type(4)));
-using F4 = float __attribute__((ext_vector_type(4)));
-using S4 = short __attribute__((ext_vector_type(4)));
-using U4 = uint32_t __attribute__((ext_vector_type(4)));
-
-constexpr int kL = 64;   // tokens of a chunk
-
-__device__ __forceinline__ F4 mfma(BF8 a, BF8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ F4 mfma1(float a, float b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
-
-// Four rows of one column for every lane: in each group of 16 lanes, lane l
-// points at columns 4 (l & 3).. of row l >> 2 and gets column l of the rows.
-__device__ __forceinline__ BF4 read_tr(const uint16_t* p) {
-  typedef __attribute__((address_space(3))) S4* L;
-  return __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
-}
-
-// Eight floats as a sum of bf16 numbers, by cutting bits off: hi holds the
-// upper 8 significant bits, mid the next 8, lo the rest rounded.
-__device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper halves of a and b
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t round2(float a, float b) {
-  using F2 = float __attribute__((ext_vector_type(2)));
-  using B2 = __bf16 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(((F2){a, b}), B2));
-}
-template <int N>
-__device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
-  float r[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = f[j];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    uint32_t d[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + 1 < N) {
-        d[j] = upper2(r[2 * j], r[2 * j + 1]);
-        r[2 * j] -= cut(r[2 * j]);
-        r[2 * j + 1] -= cut(r[2 * j + 1]);
-      } else {
-        d[j] = round2(r[2 * j], r[2 * j + 1]);
-      }
-    }
-    out[n] = __builtin_bit_cast(BF8, (U4){d[0], d[1], d[2], d[3]});
-  }
-}
-
-__device__ __forceinline__ BF8 join(BF4 a, BF4 b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// Inclusive sums over the wave's 64 lanes, by DPP moves of the two halves:
-// shifts within rows of 16, then the last lane of a row, of a half, on.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double shifted(double x) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
-  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
-}
-__device__ __forceinline__ double wave_sums(double x) {
-  x += shifted<0x111, 0xF>(x);
-  x += shifted<0x112, 0xF>(x);
-  x += shifted<0x114, 0xF>(x);
-  x += shifted<0x118, 0xF>(x);
-  x += shifted<0x142, 0xA>(x);
-  x += shifted<0x143, 0xC>(x);
-  return x;
-}
-
-// Segment s of the packed tokens.  Segment s = (sequence i, cell c) with
-// s = i + c: cells are seg tokens of the packed axis, and each sequence or
-// cell boundary moves s on by one, so (i, c) follows from s and the offsets.
-struct Segment {
-  int seq, t0, t1;      // tokens
-  bool first, last, none;
-};
-__device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int s) {
-  Segment r{0, 0, 0, true, true, false};
-  int start = 0, end = a.T;
-  if (a.offsets) {
-    const int lane = (int)(threadIdx.x & 63u);
-    int lo = 0, len = a.n - 1;              // sequences i in [1, n-1] with offsets[i] / seg + i <= s
-    while (len > 0) {
-      const int step = (len + 63) >> 6;
-      const int i = lo + (lane + 1) * step;
-      const bool le = i <= lo + len && min(max(a.offsets[i], 0), a.T) / seg + i <= s;
-      const int c = (int)__popcll(__ballot(le));
-      lo += c * step;
-      len = min(len - c * step, step - 1);
-    }
-    r.seq = __builtin_amdgcn_readfirstlane(lo);
-    start = min(max(a.offsets[r.seq], 0), a.T);
-    end = min(max(a.offsets[r.seq + 1], start), a.T);
-  }
-  const int c = s - r.seq, c0 = start / seg, c1 = end > start ? (end - 1) / seg : c0;
-  r.none = c < c0 || c > c1;
-  r.first = c == c0;
-  r.last = c == c1;
-  r.t0 = r.first ? start : c * seg;
-  r.t1 = r.last ? end : (c + 1) * seg;
-  return r;
-}
-
-// 64 rows of a bf16 tensor from row t0's element `p` on, `n` of them real: 16-byte
-// pieces of `width` elements, zeros behind the last row.  VEC: buffer loads,
-// whose bound is the last real row's end (rows are at most 2^24 elements
-// apart, so offsets fit; a piece that begins in a row begins in front of the
-// bound, and pieces are 16-byte aligned within it).
-template <bool VEC>
-struct Tile {
-  const uint16_t* p;
-  __amdgpu_buffer_rsrc_t rsrc;
-  int32_t stride, n, width;
-  __device__ __forceinline__ Tile(const void* base, int64_t at, int64_t row, int n_, int width_)
-      : p((const uint16_t*)base + at), stride((int32_t)row), n(n_), width(width_) {
-    if constexpr (VEC)
-      rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, n > 0 ? ((n - 1) * stride + width) * 2 : 0, 0x00027000);
-  }
-  __device__ __forceinline__ U4 load(int r, int c) const {
-    if constexpr (VEC) {
-      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (r * stride + c) * 2, 0, 0));
-    } else {
-      uint32_t d[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t e = (int64_t)r * stride + c + 2 * j;
-        const uint32_t lo = r < n && c + 2 * j < width ? p[e] : 0u, hi = r < n && c + 2 * j + 1 < width ? p[e + 1] : 0u;
-        d[j] = lo | (hi << 16);
-      }
-      return (U4){d[0], d[1], d[2], d[3]};
-    }
-  }
-};
-
-// The largest exponents (as 15-bit patterns without sign) of 8 bf16 numbers, by halves.
-using H2 = uint16_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ H2 largest(H2 x, U4 u) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x = __builtin_elementwise_max(x, __builtin_bit_cast(H2, u[j] & 0x7FFF7FFFu));
-  return x;
-}
-__device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
-
-template <int DK, int NV, int WAVES, bool DELTA, bool OUT, bool VEC>
+template <int DK, int NV, int WAVES, bool OUT, bool VEC>
 __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kT = 64 * WAVES;            // threads
   constexpr int kDV = 16 * NV * WAVES;      // value columns
   constexpr int kKS = DK / 32;              // steps of 32 channels
-  constexpr int kKR = DK + 8, kVR = kDV + 8, kPR = kL + 8, kAR = kL + 4;   // LDS rows: 16 bytes more than they need
+  constexpr int kKR = DK + 8, kVR = kDV + 8, kPR = kL + 8;   // LDS rows: 16 bytes more than they need
   constexpr int kKP = kL * DK / 8 / kT, kVP = kL * kDV / 8 / kT;           // 16-byte pieces a thread brings
   __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR];
   __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? kL * kKR : 8];
   __shared__ __attribute__((aligned(16))) uint16_t sv[kL * kVR];           // v, then the outputs
   __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 2 : 1][OUT ? kL * kPR : 8];   // P's two pieces
-  __shared__ __attribute__((aligned(16))) float sa[DELTA ? kL * kAR : 4];  // minus the triangle, inverted blocks
   __shared__ double sc[kL];
   __shared__ __attribute__((aligned(16))) float se[kL], sw[kL], sb[kL];    // 2^{c_i}, weight in the update, beta
-  __shared__ int sbad;
+  __shared__ int sodd;
 
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, q4 = lane >> 4;
@@ -247,36 +94,6 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
       nb = a.beta ? a.beta[(int64_t)(t + tid) * a.bs + h] : 1.0f;
     }
   };
-  // The token of a chunk (behind its first) whose v, or in the delta rule k or
-  // gates, are not finite begins a chunk of its own: a product with a zero of P
-  // or of the triangle would carry it to the tokens before it.
-  auto note_bad = [&](int n) {
-    H2 most = (H2){0, 0};
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
-    if constexpr (DELTA) {
-#pragma unroll
-      for (int i = 0; i < kKP; ++i) most = largest(most, nk[i]);
-      any = tid < kL && !(fabsf(nd) < INFINITY && fabsf(nb) < INFINITY);
-    }
-    if (!any && !odd(most)) return;
-    int bad = any && tid > 0 ? tid : kL;
-#pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int r = (i * kT + tid) / (kDV / 8);
-      if (r > 0 && odd(largest((H2){0, 0}, nv[i]))) bad = min(bad, r);
-    }
-    if constexpr (DELTA) {
-#pragma unroll
-      for (int i = 0; i < kKP; ++i) {
-        const int r = (i * kT + tid) / (DK / 8);
-        if (r > 0 && odd(largest((H2){0, 0}, nk[i]))) bad = min(bad, r);
-      }
-    }
-    if (bad < n) atomicMin(&sbad, bad);
-  };
-
   // S = 2^{c of the last token} S + sum_j k_j (w_j u_j)^T, four tiles at a time
   auto update = [&](const BF8 (&wu)[NV][2][3], float eall) {
 #pragma unroll
@@ -306,20 +123,21 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     }
   };
 
-  if (tid == 0) sbad = kL;
+  if (tid == 0) sodd = 0;
   double total = 0.0;
   fetch(sg.t0, sg.t1);
   __syncthreads();
   for (int t = sg.t0; t < sg.t1;) {
-    int n = min(kL, sg.t1 - t);
+    const int n = min(kL, sg.t1 - t);
     // ---- this chunk into LDS; gates
-    if constexpr (OUT) note_bad(n);
-    __syncthreads();                         // the chunk before has been read; sbad is known
-    const bool cutoff = OUT && sbad < n;
-    if (cutoff) {
-      n = sbad;
-      fetch(t, t + n);
+    if constexpr (OUT) {
+      H2 most = (H2){0, 0};
+#pragma unroll
+      for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
+      if (odd(most)) sodd = 1;
     }
+    __syncthreads();                         // the chunk before has been read; sodd is known
+    const bool whole = !OUT || sodd == 0;
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
       const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
@@ -337,19 +155,22 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
       sc[lane] = c;
       sb[lane] = nb;
       se[lane] = __builtin_amdgcn_exp2f((float)c);
-      sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * (DELTA ? 1.0f : nb);
+      sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * nb;
     }
     __syncthreads();
-    if (cutoff && tid == 0) sbad = kL;       // read by all, and next written behind the chunk's other barriers
+    if (OUT && tid == 0) sodd = 0;           // read by all, and next written behind the chunk's last barrier
     const int next = t + n;
     if (next < sg.t1) fetch(next, sg.t1);
     const double call = sc[kL - 1];
     total += call;
     const float eall = __builtin_amdgcn_exp2f((float)call);
 
-    F4 U[DELTA ? NV : 1][4];                 // u of the chunk's rows (delta rule)
-    if constexpr (OUT) {
-      // ---- P (transposed tiles: a lane gets 4 j of one i) and the triangle
+    if (OUT && !whole) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        by_token<DK, false, kKR, kVR>(a, t, n, h, sk, sq, sv, (wave * NV + v) * 16 + m, S[v]);
+    } else if constexpr (OUT) {
+      // ---- P (transposed tiles: a lane gets 4 j of one i)
 #pragma unroll
       for (int x = 0; x < 4 / WAVES; ++x) {
         const int it = WAVES == 4 ? wave : (x ? 3 - wave : wave);
@@ -358,20 +179,16 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
         // two tiles at a time, to the end of the step of 32 that the products below
         // read: right of the diagonal they become zeros
         for (int jp = 0; jp <= it; jp += 2) {
-          F4 p[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}}, kk[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}};
+          F4 p[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}};
 #pragma unroll
           for (int c = 0; c < kKS; ++c) {
             const BF8 qi = *(const BF8*)&sq[i * kKR + 32 * c + 8 * q4];
-            BF8 ki{};
-            if constexpr (DELTA) ki = *(const BF8*)&sk[i * kKR + 32 * c + 8 * q4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const BF8 kj = *(const BF8*)&sk[(16 * (jp + y) + m) * kKR + 32 * c + 8 * q4];
               p[y] = mfma(kj, qi, p[y]);
-              if constexpr (DELTA) kk[y] = mfma(kj, ki, kk[y]);
             }
           }
-          const float bi = sb[i];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int j = 16 * (jp + y) + 4 * q4;
@@ -380,16 +197,12 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
 #pragma unroll
             for (int r = 0; r < 4; ++r) cj[r] = sc[j + r];
             uint32_t hi[2], lo[2];
-            float f[4], tri[4];
+            float f[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float e = __builtin_amdgcn_exp2f((float)(ci - cj[r]));
-              const float w = p[y][r] * e * (DELTA ? 1.0f : bj[r]);
+              const float w = p[y][r] * e * bj[r];
               f[r] = j + r <= i ? w : 0.0f;
-              if constexpr (DELTA) {
-                const float z = -(bi * e * kk[y][r]);
-                tri[r] = j + r < i ? z : 0.0f;
-              }
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -398,39 +211,19 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
             }
             *(uint2*)&sp[0][i * kPR + j] = make_uint2(hi[0], hi[1]);
             *(uint2*)&sp[1][i * kPR + j] = make_uint2(lo[0], lo[1]);
-            if constexpr (DELTA) *(F4*)&sa[i * kAR + j] = (F4){tri[0], tri[1], tri[2], tri[3]};
           }
         }
       }
       __syncthreads();
-      if constexpr (DELTA) {
-        // the four diagonal blocks of I + A inverted by substitution, a column each lane
-        if (wave == (t / kL) % WAVES) {
-          float x[16];
-          float* blk = &sa[(16 * q4) * kAR + 16 * q4];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y = i == m ? 1.0f : 0.0f;
-#pragma unroll
-            for (int j = 0; j < i; ++j) y = fmaf(blk[i * kAR + j], x[j], y);
-            x[i] = y;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) blk[i * kAR + m] = x[i];
-        }
-      }
       // ---- products with the state
-      F4 O[NV][4], R[DELTA ? NV : 1][4];
+      F4 O[NV][4];
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          O[v][i] = (F4){0, 0, 0, 0};
-          if constexpr (DELTA) R[v][i] = (F4){0, 0, 0, 0};
-        }
+        for (int i = 0; i < 4; ++i) O[v][i] = (F4){0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < kKS; ++c) {
-        BF8 sp_[NV][DELTA ? 3 : 2];
+        BF8 sp_[NV][2];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           float f[8];
@@ -438,76 +231,33 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           for (int j = 0; j < 8; ++j) f[j] = S[v][2 * c + (j >> 2)][j & 3];
           split(f, sp_[v]);
         }
-        BF8 qf[4], kf[DELTA ? 4 : 1];
+        BF8 qf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
-          if constexpr (DELTA) kf[i] = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
-        }
+        for (int i = 0; i < 4; ++i) qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
         // products on one accumulator are kept apart: each takes several issue slots
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (x < 2) O[v][i] = mfma(qf[i], sp_[v][x < 2 ? x : 0], O[v][i]);
-              if constexpr (DELTA) R[v][i] = mfma(kf[i], sp_[v][DELTA ? x : 0], R[v][i]);
-            }
+            for (int i = 0; i < 4; ++i) O[v][i] = mfma(qf[i], sp_[v][x], O[v][i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const F4 e = *(const F4*)&se[16 * i + 4 * q4];
-        F4 bi = (F4){1, 1, 1, 1};
-        if constexpr (DELTA) bi = *(const F4*)&sb[16 * i + 4 * q4];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if constexpr (DELTA) {
-            const BF4 x = read_tr(&sv[(16 * i + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[v][i][r] = bi[r] * fmaf(-e[r], R[v][i][r], (float)x[r]);
-          }
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int r = 0; r < 4; ++r) O[v][i][r] *= e[r];
-        }
-      }
-      if constexpr (DELTA) {
-        __syncthreads();                     // the inverted blocks
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const F4 tb = *(const F4*)&sa[(16 * b + m) * kAR + 16 * b + 4 * q4];
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            U[v][b] = (F4){0, 0, 0, 0};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) U[v][b] = mfma1(tb[r], R[v][b][r], U[v][b]);
-          }
-          F4 ab[3];
-#pragma unroll
-          for (int x = b + 1; x < 4; ++x) ab[x - 1] = *(const F4*)&sa[(16 * x + m) * kAR + 16 * b + 4 * q4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int x = b + 1; x < 4; ++x)
-#pragma unroll
-              for (int v = 0; v < NV; ++v) R[v][x] = mfma1(ab[x - 1][r], U[v][b][r], R[v][x]);
-        }
       }
       // ---- outputs: P u on top
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        BF8 ub[NV][DELTA ? 2 : 1];
+        BF8 ub[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          if constexpr (DELTA) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = U[v][2 * c + (j >> 2)][j & 3];
-            split(f, ub[v]);
-          } else {
-            const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
-            ub[v][0] = join(read_tr(x), read_tr(x + 16 * kVR));
-          }
+          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
+          ub[v] = join(read_tr(x), read_tr(x + 16 * kVR));
         }
         BF8 ph[4], pl[4];
 #pragma unroll
@@ -518,12 +268,12 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           pl[i] = join(*(const BF4*)y, *(const BF4*)(y + 16));
         }
 #pragma unroll
-        for (int x = 0; x < (DELTA ? 3 : 2); ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int i = 2 * c; i < 4; ++i)
-              O[v][i] = mfma(x == 1 ? pl[i] : ph[i], ub[v][DELTA && x == 2 ? 1 : 0], O[v][i]);
+              O[v][i] = mfma(x ? pl[i] : ph[i], ub[v], O[v][i]);
       }
       // ---- the state update (below) still reads v; only then the outputs take its place
       F4 W[2][2];
@@ -543,7 +293,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float vv = (float)y[j];
-            f[j] = W[c][j >> 2][j & 3] * (DELTA ? U[DELTA ? v : 0][2 * c + (j >> 2)][j & 3] : vv);
+            f[j] = W[c][j >> 2][j & 3] * vv;
             if (a.skip) O[v][2 * c + (j >> 2)][j & 3] = fmaf(skip, vv, O[v][2 * c + (j >> 2)][j & 3]);
           }
           split(f, wu[v][c]);
@@ -558,6 +308,22 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
             sv[(16 * i + 4 * q4 + r) * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
           }
       update(wu, eall);
+    } else {
+      BF8 wu[NV][2][3];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
+          const BF8 y = join(read_tr(x), read_tr(x + 16 * kVR));
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = sw[32 * c + 16 * (j >> 2) + 4 * q4 + (j & 3)] * (float)y[j];
+          split(f, wu[v][c]);
+        }
+      update(wu, eall);
+    }
+    if constexpr (OUT) {
       __syncthreads();                       // outputs are in LDS, the chunk has been read
 #pragma unroll
       for (int i = 0; i < kVP; ++i) {
@@ -574,20 +340,6 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           }
         }
       }
-    } else {
-      BF8 wu[NV][2][3];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
-          const BF8 y = join(read_tr(x), read_tr(x + 16 * kVR));
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = sw[32 * c + 16 * (j >> 2) + 4 * q4 + (j & 3)] * (float)y[j];
-          split(f, wu[v][c]);
-        }
-      update(wu, eall);
     }
     t = next;
   }
@@ -635,25 +387,22 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
   }
 }
 
-template <int DK, int NV, int WAVES, bool DELTA, bool VEC>
+template <int DK, int NV, int WAVES, bool VEC>
 hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int vchunks = (a.dv + 16 * NV * WAVES - 1) / (16 * NV * WAVES);
   const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
-  if constexpr (!DELTA) {
-    if (g.states) {
-      k_scan_chunk<DK, NV, WAVES, false, false, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
-      const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
-      k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
-    }
+  if (g.states) {
+    k_scan_chunk<DK, NV, WAVES, false, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+    const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
+    k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
   }
-  k_scan_chunk<DK, NV, WAVES, DELTA, true, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
+  k_scan_chunk<DK, NV, WAVES, true, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
   return hipGetLastError();
 }
 
 template <int DK>
 hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  if (a.delta) return a.vec ? chunk<DK, 1, 4, true, true>(a, g, s) : chunk<DK, 1, 4, true, false>(a, g, s);
-  return a.vec ? chunk<DK, 1, 4, false, true>(a, g, s) : chunk<DK, 1, 4, false, false>(a, g, s);
+  return a.vec ? chunk<DK, 1, 4, true>(a, g, s) : chunk<DK, 1, 4, false>(a, g, s);
 }
 
 }  // namespace

@@ -1,0 +1,412 @@
+// Scan of packed bf16 prompts by the delta rule with one decay a head, 64
+// tokens at a time on the matrix cores.
+//
+// With c_i the sum of log2 decays from a chunk's first token to token i and S
+// the state before the chunk, u_i = beta_i (v_i - 2^{c_i} S k_i
+// - sum_{j<i} 2^{c_i - c_j} (k_j.k_i) u_j) is a unit lower triangular system:
+//   (I + A) U = R,  A_ij = beta_i 2^{c_i - c_j} k_j.k_i (j < i),
+//   R_i = beta_i (v_i - 2^{c_i} S k_i),  so U = T R with T = (I + A)^-1,
+//   o_i = 2^{c_i} S q_i + sum_{j<=i} P_ij u_j,  P_ij = 2^{c_i - c_j} k_j.q_i,
+//   S'  = 2^{c_last} S + sum_j 2^{c_last - c_j} u_j k_j^T.
+// T and P do not depend on the state.  A first launch makes them for all
+// chunks at once, in the layout in which the second one's lanes take them;
+// the second goes through a sequence's chunks one after the other.  That
+// chain bounds a long prompt: with T at hand a chunk is four products.
+//
+// Precision: q, k and v are bf16, so a product with one of them is exact when
+// the other operand is cut into bf16 pieces: three (24 bits) of S in S k and
+// of u in the update, two (16 bits) of S, P and u in the outputs, which are
+// rounded to bf16 at the end.  T is fp32, made and applied by fp32 matrix
+// instructions: its diagonal blocks of 16 by substitution, the others from
+// them.  c is summed in fp64; a decay of zero counts as 2^-10000.
+#include <hip/hip_runtime.h>
+
+#include "qstate_scan_tiles.hpp"
+
+namespace qs {
+namespace {
+
+// What the first launch leaves for a chunk of a head.
+constexpr int kGate = 256;                    // floats: 2^{c_i}, 2^{c_last - c_i}, beta_i, 2^{c_last}, oddness
+constexpr int kTri = 10 * 256;                // floats: T's lower tiles, a float4 a lane
+constexpr int kPieces = 6 * 2 * 64 * 8;       // bf16: P's lower 16 x 32 tiles, upper and lower halves, 8 a lane
+constexpr int kPrepFloats = kGate + kTri + kPieces / 2;
+static_assert(kPrepFloats * 4 == kScanPrepBytes, "workspace a chunk and head");
+
+__device__ __forceinline__ int tri(int b, int a) { return b * (b + 1) / 2 + a; }
+__device__ __forceinline__ int piece(int i, int c) { return i < 2 ? i : 2 * i - 2 + c; }
+
+template <int DK, bool VEC>
+__global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* prep) {
+  constexpr int kKS = DK / 32, kKR = DK + 8, kAR = kL + 4, kKP = kL * DK / 8 / 256;
+  __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR], sq[kL * kKR];
+  __shared__ __attribute__((aligned(16))) float sa[kL * kAR];   // minus A; then T
+  __shared__ double sc[kL];
+  __shared__ float sb[kL];
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, q4 = lane >> 4;
+  const int s = (int)(blockIdx.x / (uint32_t)a.H), h = (int)(blockIdx.x % (uint32_t)a.H);
+  const int kh = h / (a.H / a.G);
+  const Segment sg = find_segment(a, kL, s);
+  if (sg.none || sg.t1 <= sg.t0) return;
+  const int n = sg.t1 - sg.t0;
+  float* out = prep + (int64_t)blockIdx.x * kPrepFloats;
+  const Tile<VEC> tk(a.k, (int64_t)sg.t0 * a.ks + (int64_t)kh * DK, a.ks, n, DK);
+  const Tile<VEC> tq(a.q, (int64_t)sg.t0 * a.qs + (int64_t)kh * DK, a.qs, n, DK);
+#pragma unroll
+  for (int i = 0; i < kKP; ++i) {
+    const int p = i * 256 + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
+    *(U4*)&sk[r * kKR + c] = tk.load(r, c);
+    *(U4*)&sq[r * kKR + c] = tq.load(r, c);
+  }
+  if (wave == 0) {
+    float d = 1.0f, b = 0.0f;
+    if (lane < n) {
+      d = a.decay[(int64_t)(sg.t0 + lane) * a.ds + h];
+      b = a.beta ? a.beta[(int64_t)(sg.t0 + lane) * a.bs + h] : 1.0f;
+    }
+    const double c = wave_sums(d == 0.0f ? -10000.0 : (double)log2f(d));
+    const double all = __shfl(c, 63);
+    sc[lane] = c;
+    sb[lane] = b;
+    out[lane] = __builtin_amdgcn_exp2f((float)c);
+    out[64 + lane] = __builtin_amdgcn_exp2f((float)(all - c));
+    out[128 + lane] = b;
+    const bool odd_gate = __ballot(!(fabsf(d) < INFINITY && fabsf(b) < INFINITY)) != 0;
+    if (lane == 0) {
+      out[192] = __builtin_amdgcn_exp2f((float)all);
+      out[193] = odd_gate ? 1.0f : 0.0f;
+    }
+  }
+  __syncthreads();
+  // ---- P and A, transposed tiles: a lane gets 4 j of one i; wave i takes rows 16 i ..
+  {
+    const int i = 16 * wave + m;
+    const double ci = sc[i];
+    const float bi = sb[i];
+    for (int jp = 0; jp <= wave; jp += 2) {
+      F4 p[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}}, kk[2] = {(F4){0, 0, 0, 0}, (F4){0, 0, 0, 0}};
+#pragma unroll
+      for (int c = 0; c < kKS; ++c) {
+        const BF8 qi = *(const BF8*)&sq[i * kKR + 32 * c + 8 * q4], ki = *(const BF8*)&sk[i * kKR + 32 * c + 8 * q4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const BF8 kj = *(const BF8*)&sk[(16 * (jp + y) + m) * kKR + 32 * c + 8 * q4];
+          p[y] = mfma(kj, qi, p[y]);
+          kk[y] = mfma(kj, ki, kk[y]);
+        }
+      }
+      U4 hi, lo;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int j = 16 * (jp + y) + 4 * q4;
+        float f[4];
+        F4 neg;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f((float)(ci - sc[j + r]));
+          const float w = p[y][r] * e, z = -(bi * e * kk[y][r]);
+          f[r] = j + r <= i ? w : 0.0f;
+          neg[r] = j + r < i ? z : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          hi[2 * y + r] = upper2(f[2 * r], f[2 * r + 1]);
+          lo[2 * y + r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
+        }
+        *(F4*)&sa[i * kAR + j] = neg;
+      }
+      U4* to = (U4*)(out + kGate + kTri) + piece(wave, jp >> 1) * 128 + lane;
+      to[0] = hi;
+      to[64] = lo;
+    }
+  }
+  __syncthreads();
+  // ---- the diagonal blocks of I + A inverted, a column each lane
+  if (wave == 0) {
+    float x[16];
+    float* blk = &sa[(16 * q4) * kAR + 16 * q4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float y = i == m ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) y = fmaf(blk[i * kAR + j], x[j], y);
+      x[i] = y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) blk[i * kAR + m] = x[i];
+  }
+  __syncthreads();
+  // ---- T's column of blocks `wave`: T_ba = T_bb sum_{a<=x<b} (-A_bx) T_xa
+  F4 X[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) X[b] = (F4){0, 0, 0, 0};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (b == wave) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[b][r] = sa[(16 * b + 4 * q4 + r) * kAR + 16 * b + m];
+    } else if (b > wave) {
+      F4 acc = (F4){0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < b; ++x) {            // blocks before the column are zero
+        const F4 ab = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
+        if (x >= wave)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc = mfma1(ab[r], X[x][r], acc);
+      }
+      const F4 tb = *(const F4*)&sa[(16 * b + m) * kAR + 16 * b + 4 * q4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[b] = mfma1(tb[r], acc[r], X[b]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b > wave)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sa[(16 * b + 4 * q4 + r) * kAR + 16 * wave + m] = X[b][r];
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int x = 0; x <= b; ++x)
+      if (tri(b, x) % 4 == wave)
+        *((F4*)(out + kGate) + tri(b, x) * 64 + lane) = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
+}
+
+// One sequence's chunks in order; a workgroup holds 16 WAVES value columns of a
+// head, each wave 16 in accumulators [dk][v] (rows dealt so that a lane holds 8
+// channels in a row, the second operand of S k and S q as it is).
+template <int DK, int WAVES, bool VEC>
+__global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int vchunks) {
+  constexpr int kT = 64 * WAVES, kDV = 16 * WAVES, kKS = DK / 32, kKR = DK + 8, kVR = kDV + 8;
+  constexpr int kKP = kL * DK / 8 / kT, kVP = kL * kDV / 8 / kT;
+  __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR], sq[kL * kKR], sv[kL * kVR];
+  __shared__ __attribute__((aligned(16))) float sgate[kGate];
+  __shared__ int sodd;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, q4 = lane >> 4;
+  const int per = a.H * vchunks;
+  const int seq = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
+  const int h = hv / vchunks, v0 = (hv % vchunks) * kDV, kh = h / (a.H / a.G);
+  const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
+  const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
+  const int64_t head = (int64_t)h * a.dv, st = (int64_t)seq * a.H * a.dv;
+  const int col = wave * 16 + m, v = v0 + col;
+
+  F4 S[2 * kKS];
+#pragma unroll
+  for (int t = 0; t < 2 * kKS; ++t) {
+    S[t] = (F4){0, 0, 0, 0};
+    if (a.initial && v < a.dv)
+      S[t] = *(const F4*)(a.initial + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
+  }
+  U4 nk[kKP], nq[kKP], nv[kVP];
+  float ng = 0.0f;
+  const float* np = nullptr;                 // the next chunk's T, P and gates
+  auto fetch = [&](int t, int t1) {
+    const int rows = t1 - t;
+    const Tile<VEC> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
+    const Tile<VEC> tq(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK);
+    const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) {
+      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
+      nk[i] = tk.load(r, c);
+      nq[i] = tq.load(r, c);
+    }
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+      nv[i] = tv.load(r, c);
+    }
+    np = prep + ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats;
+    if (tid < 194) ng = np[tid];
+  };
+  const float skip = a.skip ? a.skip[h] : 0.0f;
+  if (tid == 0) sodd = 0;
+  if (start < end) fetch(start, min((start / kL + 1) * kL, end));
+  __syncthreads();
+  for (int t = start; t < end;) {
+    const int next = min((t / kL + 1) * kL, end), n = next - t;
+    H2 most = (H2){0, 0};
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) most = largest(most, nk[i]);
+    if (odd(most) || (tid == 193 && ng != 0.0f)) sodd = 1;
+    __syncthreads();                         // the chunk before has been read; sodd is known
+    const bool whole = sodd == 0;
+#pragma unroll
+    for (int i = 0; i < kKP; ++i) {
+      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
+      *(U4*)&sk[r * kKR + c] = nk[i];
+      *(U4*)&sq[r * kKR + c] = nq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+      *(U4*)&sv[r * kVR + c] = nv[i];
+    }
+    if (tid < 194) sgate[tid] = ng;
+    __syncthreads();
+    if (tid == 0) sodd = 0;                  // read by all, and next written behind the chunk's last barrier
+    // T and P into registers: they are needed behind the products with the state
+    F4 T[10];
+    BF8 P[6][2];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) T[i] = *((const F4*)(np + kGate) + i * 64 + lane);
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) P[i][j] = *((const BF8*)(np + kGate + kTri) + (2 * i + j) * 64 + lane);
+    if (next < end) fetch(next, min(next + kL, end));
+    if (!whole) {
+      by_token<DK, true, kKR, kVR>(a, t, n, h, sk, sq, sv, col, S);
+    } else {
+      // ---- products with the state
+      F4 O[4], R[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[i] = R[i] = (F4){0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kKS; ++c) {
+        BF8 sp[3];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = S[2 * c + (j >> 2)][j & 3];
+        split(f, sp);
+        BF8 qf[4], kf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          kf[i] = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
+          qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
+        }
+        // products on one accumulator are kept apart: each takes several issue slots
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            R[i] = mfma(kf[i], sp[x], R[i]);
+            if (x < 2) O[i] = mfma(qf[i], sp[x], O[i]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F4 e = *(const F4*)&sgate[16 * i + 4 * q4], b = *(const F4*)&sgate[128 + 16 * i + 4 * q4];
+        const BF4 x = read_tr(&sv[(16 * i + 4 * q4 + (m >> 2)) * kVR + wave * 16 + 4 * (m & 3)]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          R[i][r] = b[r] * fmaf(-e[r], R[i][r], (float)x[r]);
+          O[i][r] *= e[r];
+          if (a.skip) O[i][r] = fmaf(skip, (float)x[r], O[i][r]);
+        }
+      }
+      // ---- U = T R
+      F4 U[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) U[i] = (F4){0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int b = x; b < 4; ++b) U[b] = mfma1(T[tri(b, x)][r], R[x][r], U[b]);
+      // ---- outputs: P u on top; they take v's place
+      BF8 wu[2][3];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float f[8], g[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const F4 w = *(const F4*)&sgate[64 + 32 * c + 16 * j + 4 * q4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            f[4 * j + r] = U[2 * c + j][r];
+            g[4 * j + r] = U[2 * c + j][r] * w[r];
+          }
+        }
+        BF8 ub[2];
+        split(f, ub);
+        split(g, wu[c]);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int i = 2 * c; i < 4; ++i) O[i] = mfma(P[piece(i, c)][x == 1], ub[x == 2], O[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const __bf16 y = (__bf16)O[i][r];
+          sv[(16 * i + 4 * q4 + r) * kVR + col] = __builtin_bit_cast(uint16_t, y);
+        }
+      // ---- the state
+      const float eall = sgate[192];
+#pragma unroll
+      for (int t4 = 0; t4 < 2 * kKS; t4 += 4) {
+#pragma unroll
+        for (int x = t4; x < t4 + 4; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[x][r] *= eall;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          BF8 kt[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint16_t* p =
+                &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * ((t4 + x) >> 1) + 8 * (m & 3) + 4 * (x & 1)];
+            kt[x] = join(read_tr(p), read_tr(p + 16 * kKR));
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[t4 + x] = mfma(kt[x], wu[c][p], S[t4 + x]);
+        }
+      }
+    }
+    __syncthreads();                         // outputs are in LDS, the chunk has been read
+#pragma unroll
+    for (int i = 0; i < kVP; ++i) {
+      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
+      if (r < n) {
+        const U4 y = *(const U4*)&sv[r * kVR + c];
+        uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
+        if constexpr (VEC) {
+          if (v0 + c < a.dv) *(U4*)(o + c) = y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (v0 + c + j < a.dv) o[c + j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+        }
+      }
+    }
+    t = next;
+  }
+  if (v < a.dv)
+#pragma unroll
+    for (int t = 0; t < 2 * kKS; ++t)
+      *(F4*)(a.final + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1)) = S[t];
+}
+
+template <int DK, bool VEC>
+hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  constexpr int WAVES = 4;
+  const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
+  k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
+  k_delta_scan<DK, WAVES, VEC><<<dim3((uint32_t)(a.n * a.H * vchunks)), 64 * WAVES, 0, s>>>(a, g.states, vchunks);
+  return hipGetLastError();
+}
+
+template <int DK>
+hipError_t delta_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.vec ? delta<DK, true>(a, g, s) : delta<DK, false>(a, g, s);
+}
+
+}  // namespace
+
+hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.dk == 64 ? delta_dk<64>(a, g, s) : a.dk == 128 ? delta_dk<128>(a, g, s) : delta_dk<256>(a, g, s);
+}
+
+}  // namespace qs

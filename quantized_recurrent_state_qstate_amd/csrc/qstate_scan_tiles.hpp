@@ -1,0 +1,208 @@
+// Device helpers of the chunked scans: bf16 and fp32 matrix instructions,
+// fp32 numbers as sums of bf16 ones, tiles of rows from global memory and in
+// LDS, sums over a wave, segments of packed tokens.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "qstate_ops.hpp"
+
+namespace qs {
+namespace {
+
+using BF8 = __bf16 __attribute__((ext_vector_type(8)));
+using BF4 = __bf16 __attribute__((ext_vector_type(4)));
+using F4 = float __attribute__((ext_vector_type(4)));
+using S4 = short __attribute__((ext_vector_type(4)));
+using U4 = uint32_t __attribute__((ext_vector_type(4)));
+
+constexpr int kL = 64;   // tokens of a chunk
+
+__device__ __forceinline__ F4 mfma(BF8 a, BF8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mfma1(float a, float b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// Four rows of one column for every lane: in each group of 16 lanes, lane l
+// points at columns 4 (l & 3).. of row l >> 2 and gets column l of the rows.
+__device__ __forceinline__ BF4 read_tr(const uint16_t* p) {
+  typedef __attribute__((address_space(3))) S4* L;
+  return __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
+}
+
+// Eight floats as a sum of bf16 numbers, by cutting bits off: hi holds the
+// upper 8 significant bits, mid the next 8, lo the rest rounded.
+__device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper halves of a and b
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  using F2 = float __attribute__((ext_vector_type(2)));
+  using B2 = __bf16 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(((F2){a, b}), B2));
+}
+template <int N>
+__device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = f[j];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + 1 < N) {
+        d[j] = upper2(r[2 * j], r[2 * j + 1]);
+        r[2 * j] -= cut(r[2 * j]);
+        r[2 * j + 1] -= cut(r[2 * j + 1]);
+      } else {
+        d[j] = round2(r[2 * j], r[2 * j + 1]);
+      }
+    }
+    out[n] = __builtin_bit_cast(BF8, (U4){d[0], d[1], d[2], d[3]});
+  }
+}
+
+__device__ __forceinline__ BF8 join(BF4 a, BF4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Inclusive sums over the wave's 64 lanes, by DPP moves of the two halves:
+// shifts within rows of 16, then the last lane of a row, of a half, on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ double wave_sums(double x) {
+  x += shifted<0x111, 0xF>(x);
+  x += shifted<0x112, 0xF>(x);
+  x += shifted<0x114, 0xF>(x);
+  x += shifted<0x118, 0xF>(x);
+  x += shifted<0x142, 0xA>(x);
+  x += shifted<0x143, 0xC>(x);
+  return x;
+}
+
+// Segment s of the packed tokens.  Segment s = (sequence i, cell c) with
+// s = i + c: cells are seg tokens of the packed axis, and each sequence or
+// cell boundary moves s on by one, so (i, c) follows from s and the offsets.
+struct Segment {
+  int seq, t0, t1;      // tokens
+  bool first, last, none;
+};
+__device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int s) {
+  Segment r{0, 0, 0, true, true, false};
+  int start = 0, end = a.T;
+  if (a.offsets) {
+    const int lane = (int)(threadIdx.x & 63u);
+    int lo = 0, len = a.n - 1;              // sequences i in [1, n-1] with offsets[i] / seg + i <= s
+    while (len > 0) {
+      const int step = (len + 63) >> 6;
+      const int i = lo + (lane + 1) * step;
+      const bool le = i <= lo + len && min(max(a.offsets[i], 0), a.T) / seg + i <= s;
+      const int c = (int)__popcll(__ballot(le));
+      lo += c * step;
+      len = min(len - c * step, step - 1);
+    }
+    r.seq = __builtin_amdgcn_readfirstlane(lo);
+    start = min(max(a.offsets[r.seq], 0), a.T);
+    end = min(max(a.offsets[r.seq + 1], start), a.T);
+  }
+  const int c = s - r.seq, c0 = start / seg, c1 = end > start ? (end - 1) / seg : c0;
+  r.none = c < c0 || c > c1;
+  r.first = c == c0;
+  r.last = c == c1;
+  r.t0 = r.first ? start : c * seg;
+  r.t1 = r.last ? end : (c + 1) * seg;
+  return r;
+}
+
+// 64 rows of a bf16 tensor from row t0's element `p` on, `n` of them real: 16-byte
+// pieces of `width` elements, zeros behind the last row.  VEC: buffer loads,
+// whose bound is the last real row's end (rows are at most 2^24 elements
+// apart, so offsets fit; a piece that begins in a row begins in front of the
+// bound, and pieces are 16-byte aligned within it).
+template <bool VEC>
+struct Tile {
+  const uint16_t* p;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int32_t stride, n, width;
+  __device__ __forceinline__ Tile(const void* base, int64_t at, int64_t row, int n_, int width_)
+      : p((const uint16_t*)base + at), stride((int32_t)row), n(n_), width(width_) {
+    if constexpr (VEC)
+      rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, n > 0 ? ((n - 1) * stride + width) * 2 : 0, 0x00027000);
+  }
+  __device__ __forceinline__ U4 load(int r, int c) const {
+    if constexpr (VEC) {
+      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (r * stride + c) * 2, 0, 0));
+    } else {
+      uint32_t d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t e = (int64_t)r * stride + c + 2 * j;
+        const uint32_t lo = r < n && c + 2 * j < width ? p[e] : 0u, hi = r < n && c + 2 * j + 1 < width ? p[e + 1] : 0u;
+        d[j] = lo | (hi << 16);
+      }
+      return (U4){d[0], d[1], d[2], d[3]};
+    }
+  }
+};
+
+// The largest exponents (as 15-bit patterns without sign) of 8 bf16 numbers, by halves.
+using H2 = uint16_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ H2 largest(H2 x, U4 u) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x = __builtin_elementwise_max(x, __builtin_bit_cast(H2, u[j] & 0x7FFF7FFFu));
+  return x;
+}
+__device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
+
+// A chunk token by token, for one with a value that is not finite: in the
+// products of a whole chunk a zero times such a value would reach the tokens
+// before it.  The state tiles are those of the scans (lane m, q4: column m,
+// channels 32 i + 8 q4 .. + 7); k, q and v lie in LDS with rows of KR and VR
+// elements, and the outputs take v's place.
+template <int DK, bool DELTA, int KR, int VR>
+__device__ __forceinline__ void by_token(const ScanArgs& a, int t, int n, int h, const uint16_t* sk, const uint16_t* sq,
+                                         uint16_t* sv, int col, F4 (&S)[DK / 16]) {
+  const int lane = (int)threadIdx.x & 63, q4 = lane >> 4;
+  const float skip = a.skip ? a.skip[h] : 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const float d = a.decay[(int64_t)(t + i) * a.ds + h], beta = a.beta ? a.beta[(int64_t)(t + i) * a.bs + h] : 1.0f;
+    const float v = __uint_as_float((uint32_t)sv[i * VR + col] << 16);
+    float w = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int c = 0; c < DK / 32; ++c) {
+      const BF8 k = *(const BF8*)&sk[i * KR + 32 * c + 8 * q4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = S[2 * c + (j >> 2)][j & 3] * d;
+        S[2 * c + (j >> 2)][j & 3] = x;
+        if constexpr (DELTA) w = fmaf(x, (float)k[j], w);
+      }
+    }
+    if constexpr (DELTA) {
+      w += __shfl_xor(w, 16);
+      w += __shfl_xor(w, 32);
+    }
+    const float u = beta * (v - w);
+#pragma unroll
+    for (int c = 0; c < DK / 32; ++c) {
+      const BF8 k = *(const BF8*)&sk[i * KR + 32 * c + 8 * q4], q = *(const BF8*)&sq[i * KR + 32 * c + 8 * q4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = fmaf(u, (float)k[j], S[2 * c + (j >> 2)][j & 3]);
+        S[2 * c + (j >> 2)][j & 3] = x;
+        o = fmaf(x, (float)q[j], o);
+      }
+    }
+    o += __shfl_xor(o, 16);
+    o += __shfl_xor(o, 32);
+    if (a.skip) o = fmaf(skip, v, o);
+    const __bf16 y = (__bf16)o;
+    if (q4 == 0) sv[i * VR + col] = __builtin_bit_cast(uint16_t, y);
+  }
+}
+
+}  // namespace
+}  // namespace qs
