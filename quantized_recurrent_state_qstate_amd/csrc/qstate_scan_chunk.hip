@@ -168,7 +168,15 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     if (OUT && !whole) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        by_token<DK, false, kKR, kVR>(a, t, n, h, sk, sq, sv, (wave * NV + v) * 16 + m, S[v]);
+        by_token<DK, false>(
+            a, t, n, h, [&](int i, int c) { return *(const BF8*)&sk[i * kKR + c]; },
+            [&](int i, int c) { return *(const BF8*)&sq[i * kKR + c]; },
+            [&](int i) { return __uint_as_float((uint32_t)sv[i * kVR + (wave * NV + v) * 16 + m] << 16); },
+            [&](int i, float o) {
+              const __bf16 y = (__bf16)o;
+              sv[i * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+            },
+            S[v]);
     } else if constexpr (OUT) {
       // ---- P (transposed tiles: a lane gets 4 j of one i)
 #pragma unroll

@@ -21,6 +21,8 @@
 // them.  c is summed in fp64; a decay of zero counts as 2^-10000.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "qstate_scan_tiles.hpp"
 
 namespace qs {
@@ -42,7 +44,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
   __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR], sq[kL * kKR];
   __shared__ __attribute__((aligned(16))) float sa[kL * kAR];   // minus A; then T
   __shared__ double sc[kL];
-  __shared__ float sb[kL];
+  __shared__ float sb[kL], sodd;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, q4 = lane >> 4;
   const int s = (int)(blockIdx.x / (uint32_t)a.H), h = (int)(blockIdx.x % (uint32_t)a.H);
@@ -53,12 +55,18 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
   float* out = prep + (int64_t)blockIdx.x * kPrepFloats;
   const Tile<VEC> tk(a.k, (int64_t)sg.t0 * a.ks + (int64_t)kh * DK, a.ks, n, DK);
   const Tile<VEC> tq(a.q, (int64_t)sg.t0 * a.qs + (int64_t)kh * DK, a.qs, n, DK);
+  if (tid == 0) sodd = 0.0f;
+  __syncthreads();
+  H2 most = (H2){0, 0};
 #pragma unroll
   for (int i = 0; i < kKP; ++i) {
     const int p = i * 256 + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-    *(U4*)&sk[r * kKR + c] = tk.load(r, c);
+    const U4 k = tk.load(r, c);
+    most = largest(most, k);
+    *(U4*)&sk[r * kKR + c] = k;
     *(U4*)&sq[r * kKR + c] = tq.load(r, c);
   }
+  if (odd(most)) sodd = 1.0f;
   if (wave == 0) {
     float d = 1.0f, b = 0.0f;
     if (lane < n) {
@@ -72,13 +80,11 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
     out[lane] = __builtin_amdgcn_exp2f((float)c);
     out[64 + lane] = __builtin_amdgcn_exp2f((float)(all - c));
     out[128 + lane] = b;
-    const bool odd_gate = __ballot(!(fabsf(d) < INFINITY && fabsf(b) < INFINITY)) != 0;
-    if (lane == 0) {
-      out[192] = __builtin_amdgcn_exp2f((float)all);
-      out[193] = odd_gate ? 1.0f : 0.0f;
-    }
+    if (!(fabsf(d) < INFINITY && fabsf(b) < INFINITY)) sodd = 1.0f;
+    if (lane == 0) out[192] = __builtin_amdgcn_exp2f((float)all);
   }
   __syncthreads();
+  if (tid == 0) out[193] = sodd;            // k or a gate is not finite
   // ---- P and A, transposed tiles: a lane gets 4 j of one i; wave i takes rows 16 i ..
   {
     const int i = 16 * wave + m;
@@ -175,25 +181,36 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
         *((F4*)(out + kGate) + tri(b, x) * 64 + lane) = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
 }
 
+// A chunk of a workgroup's columns in LDS.
+template <int DK, int DV>
+struct Chunk {
+  uint16_t k[kL * DK], q[kL * DK], v[kL * DV];   // rows as at<>() lays them
+  float prep[kPrepFloats];
+};
+
 // One sequence's chunks in order; a workgroup holds 16 WAVES value columns of a
 // head, each wave 16 in accumulators [dk][v] (rows dealt so that a lane holds 8
-// channels in a row, the second operand of S k and S q as it is).
+// channels in a row, the second operand of S k and S q as it is).  While a
+// chunk is worked on, the next one is on its way into the other buffer, from
+// memory to LDS directly; a chunk costs one barrier.
 template <int DK, int WAVES, bool VEC>
 __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int vchunks) {
-  constexpr int kT = 64 * WAVES, kDV = 16 * WAVES, kKS = DK / 32, kKR = DK + 8, kVR = kDV + 8;
-  constexpr int kKP = kL * DK / 8 / kT, kVP = kL * kDV / 8 / kT;
-  __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR], sq[kL * kKR], sv[kL * kVR];
-  __shared__ __attribute__((aligned(16))) float sgate[kGate];
-  __shared__ int sodd;
+  constexpr int kDV = 16 * WAVES, kKS = DK / 32;
+  using Buf = Chunk<DK, kDV>;
+  constexpr bool kTwo = 2 * sizeof(Buf) + WAVES * kL * 32 <= 160 * 1024;   // room for two buffers
+  __shared__ __attribute__((aligned(1024))) Buf buf0;
+  __shared__ __attribute__((aligned(1024))) typename std::conditional<kTwo, Buf, int>::type buf1;
+  __shared__ __attribute__((aligned(16))) uint16_t so[WAVES][kL * 16];     // a wave's outputs
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, q4 = lane >> 4;
   const int per = a.H * vchunks;
   const int seq = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
-  const int h = hv / vchunks, v0 = (hv % vchunks) * kDV, kh = h / (a.H / a.G);
+  const int h = hv % a.H, v0 = hv / a.H * kDV, kh = h / (a.H / a.G);
   const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
   const int64_t head = (int64_t)h * a.dv, st = (int64_t)seq * a.H * a.dv;
   const int col = wave * 16 + m, v = v0 + col;
+  const float skip = a.skip ? a.skip[h] : 0.0f;
 
   F4 S[2 * kKS];
 #pragma unroll
@@ -202,196 +219,217 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     if (a.initial && v < a.dv)
       S[t] = *(const F4*)(a.initial + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
   }
-  U4 nk[kKP], nq[kKP], nv[kVP];
-  float ng = 0.0f;
-  const float* np = nullptr;                 // the next chunk's T, P and gates
-  auto fetch = [&](int t, int t1) {
+
+  // The chunk from token t to t1 on its way into b.
+  auto fetch = [&](Buf& b, int t, int t1) {
     const int rows = t1 - t;
     const Tile<VEC> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
     const Tile<VEC> tq(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK);
     const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
+    const float* p = prep + ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats;
 #pragma unroll
-    for (int i = 0; i < kKP; ++i) {
-      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-      nk[i] = tk.load(r, c);
-      nq[i] = tq.load(r, c);
+    for (int i = 0; i < kL * DK / 512 / WAVES; ++i) {
+      const int e = (i * WAVES + wave) * 512;                       // the wave's 1 KB piece of the tile
+      tk.template bring<DK>(b.k, e, lane);
+      tq.template bring<DK>(b.q, e, lane);
     }
 #pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      nv[i] = tv.load(r, c);
+    for (int i = 0; i < kL * kDV / 512 / WAVES; ++i) tv.template bring<kDV>(b.v, (i * WAVES + wave) * 512, lane);
+    const Tile<true> tp(p, 0, 0, 1, kPrepFloats * 2);
+#pragma unroll
+    for (int i = 0; i < (kPrepFloats / 256 + WAVES - 1) / WAVES; ++i) {
+      const int e = i * WAVES + wave;
+      if (e < kPrepFloats / 256) to_lds(tp.rsrc, (uint16_t*)b.prep + e * 512, e * 1024 + lane * 16);
     }
-    np = prep + ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats;
-    if (tid < 194) ng = np[tid];
   };
-  const float skip = a.skip ? a.skip[h] : 0.0f;
-  if (tid == 0) sodd = 0;
-  if (start < end) fetch(start, min((start / kL + 1) * kL, end));
-  __syncthreads();
-  for (int t = start; t < end;) {
-    const int next = min((t / kL + 1) * kL, end), n = next - t;
-    H2 most = (H2){0, 0};
+
+  int done_t = 0, done_n = 0;                // the chunk whose outputs wait in `so`
+  auto put_out = [&]() {
 #pragma unroll
-    for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
-#pragma unroll
-    for (int i = 0; i < kKP; ++i) most = largest(most, nk[i]);
-    if (odd(most) || (tid == 193 && ng != 0.0f)) sodd = 1;
-    __syncthreads();                         // the chunk before has been read; sodd is known
-    const bool whole = sodd == 0;
-#pragma unroll
-    for (int i = 0; i < kKP; ++i) {
-      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-      *(U4*)&sk[r * kKR + c] = nk[i];
-      *(U4*)&sq[r * kKR + c] = nq[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      *(U4*)&sv[r * kVR + c] = nv[i];
-    }
-    if (tid < 194) sgate[tid] = ng;
-    __syncthreads();
-    if (tid == 0) sodd = 0;                  // read by all, and next written behind the chunk's last barrier
-    // T and P into registers: they are needed behind the products with the state
-    F4 T[10];
-    BF8 P[6][2];
-#pragma unroll
-    for (int i = 0; i < 10; ++i) T[i] = *((const F4*)(np + kGate) + i * 64 + lane);
-#pragma unroll
-    for (int i = 0; i < 6; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) P[i][j] = *((const BF8*)(np + kGate + kTri) + (2 * i + j) * 64 + lane);
-    if (next < end) fetch(next, min(next + kL, end));
-    if (!whole) {
-      by_token<DK, true, kKR, kVR>(a, t, n, h, sk, sq, sv, col, S);
-    } else {
-      // ---- products with the state
-      F4 O[4], R[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) O[i] = R[i] = (F4){0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < kKS; ++c) {
-        BF8 sp[3];
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = S[2 * c + (j >> 2)][j & 3];
-        split(f, sp);
-        BF8 qf[4], kf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kf[i] = *(const BF8*)&sk[(16 * i + m) * kKR + 32 * c + 8 * q4];
-          qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
-        }
-        // products on one accumulator are kept apart: each takes several issue slots
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            R[i] = mfma(kf[i], sp[x], R[i]);
-            if (x < 2) O[i] = mfma(qf[i], sp[x], O[i]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F4 e = *(const F4*)&sgate[16 * i + 4 * q4], b = *(const F4*)&sgate[128 + 16 * i + 4 * q4];
-        const BF4 x = read_tr(&sv[(16 * i + 4 * q4 + (m >> 2)) * kVR + wave * 16 + 4 * (m & 3)]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          R[i][r] = b[r] * fmaf(-e[r], R[i][r], (float)x[r]);
-          O[i][r] *= e[r];
-          if (a.skip) O[i][r] = fmaf(skip, (float)x[r], O[i][r]);
-        }
-      }
-      // ---- U = T R
-      F4 U[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) U[i] = (F4){0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int b = x; b < 4; ++b) U[b] = mfma1(T[tri(b, x)][r], R[x][r], U[b]);
-      // ---- outputs: P u on top; they take v's place
-      BF8 wu[2][3];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float f[8], g[8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const F4 w = *(const F4*)&sgate[64 + 32 * c + 16 * j + 4 * q4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            f[4 * j + r] = U[2 * c + j][r];
-            g[4 * j + r] = U[2 * c + j][r] * w[r];
-          }
-        }
-        BF8 ub[2];
-        split(f, ub);
-        split(g, wu[c]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-#pragma unroll
-          for (int i = 2 * c; i < 4; ++i) O[i] = mfma(P[piece(i, c)][x == 1], ub[x == 2], O[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const __bf16 y = (__bf16)O[i][r];
-          sv[(16 * i + 4 * q4 + r) * kVR + col] = __builtin_bit_cast(uint16_t, y);
-        }
-      // ---- the state
-      const float eall = sgate[192];
-#pragma unroll
-      for (int t4 = 0; t4 < 2 * kKS; t4 += 4) {
-#pragma unroll
-        for (int x = t4; x < t4 + 4; ++x)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[x][r] *= eall;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          BF8 kt[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint16_t* p =
-                &sk[(32 * c + 4 * q4 + (m >> 2)) * kKR + 32 * ((t4 + x) >> 1) + 8 * (m & 3) + 4 * (x & 1)];
-            kt[x] = join(read_tr(p), read_tr(p + 16 * kKR));
-          }
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) S[t4 + x] = mfma(kt[x], wu[c][p], S[t4 + x]);
-        }
-      }
-    }
-    __syncthreads();                         // outputs are in LDS, the chunk has been read
-#pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      if (r < n) {
-        const U4 y = *(const U4*)&sv[r * kVR + c];
-        uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
+    for (int i = 0; i < 2; ++i) {
+      const int r = 32 * i + (lane >> 1), c = 8 * (lane & 1);
+      if (r < done_n) {
+        const U4 y = *(const U4*)&so[wave][r * 16 + c];
+        uint16_t* o = (uint16_t*)a.out + (int64_t)(done_t + r) * a.os + head + v0 + wave * 16 + c;
         if constexpr (VEC) {
-          if (v0 + c < a.dv) *(U4*)(o + c) = y;
+          if (v0 + wave * 16 + c < a.dv) *(U4*)o = y;
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (v0 + c + j < a.dv) o[c + j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+            if (v0 + wave * 16 + c + j < a.dv) o[j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
         }
       }
     }
+  };
+
+  auto work = [&](Buf& b, int t, int n) {
+    // ---- v of the wave's columns; a value that is not finite
+    BF4 x[4];
+    H2 most = (H2){0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = read_tr(&b.v[at<kDV>(16 * i + 4 * q4 + (m >> 2), wave * 16 + 4 * (m & 3))]);
+      const uint2 u = __builtin_bit_cast(uint2, x[i]);
+      most = largest(most, (U4){u.x, u.y, 0, 0});
+    }
+    if (b.prep[193] != 0.0f || __ballot(odd(most)) != 0) {
+      by_token<DK, true>(
+          a, t, n, h, [&](int i, int c) { return *(const BF8*)&b.k[at<DK>(i, c)]; },
+          [&](int i, int c) { return *(const BF8*)&b.q[at<DK>(i, c)]; },
+          [&](int i) { return __uint_as_float((uint32_t)b.v[at<kDV>(i, col)] << 16); },
+          [&](int i, float o) {
+            const __bf16 y = (__bf16)o;
+            so[wave][i * 16 + m] = __builtin_bit_cast(uint16_t, y);
+          },
+          S);
+      return;
+    }
+    // ---- products with the state
+    F4 O[4], R[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) O[i] = R[i] = (F4){0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < kKS; ++c) {
+      BF8 sp[3];
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = S[2 * c + (j >> 2)][j & 3];
+      split(f, sp);
+      BF8 qf[4], kf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kf[i] = *(const BF8*)&b.k[at<DK>(16 * i + m, 32 * c + 8 * q4)];
+        qf[i] = *(const BF8*)&b.q[at<DK>(16 * i + m, 32 * c + 8 * q4)];
+      }
+      // products on one accumulator are kept apart: each takes several issue slots
+#pragma unroll
+      for (int y = 0; y < 3; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          R[i] = mfma(kf[i], sp[y], R[i]);
+          if (y < 2) O[i] = mfma(qf[i], sp[y], O[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F4 e = *(const F4*)&b.prep[16 * i + 4 * q4], bt = *(const F4*)&b.prep[128 + 16 * i + 4 * q4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        R[i][r] = bt[r] * fmaf(-e[r], R[i][r], (float)x[i][r]);
+        O[i][r] *= e[r];
+        if (a.skip) O[i][r] = fmaf(skip, (float)x[i][r], O[i][r]);
+      }
+    }
+    // ---- U = T R
+    F4 U[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) U[i] = (F4){0, 0, 0, 0};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      F4 T[4];
+#pragma unroll
+      for (int i = y; i < 4; ++i) T[i] = *(const F4*)&b.prep[kGate + tri(i, y) * 256 + lane * 4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = y; i < 4; ++i) U[i] = mfma1(T[i][r], R[y][r], U[i]);
+    }
+    // ---- outputs: P u on top
+    BF8 wu[2][3];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float f[8], g[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const F4 w = *(const F4*)&b.prep[64 + 32 * c + 16 * j + 4 * q4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[4 * j + r] = U[2 * c + j][r];
+          g[4 * j + r] = U[2 * c + j][r] * w[r];
+        }
+      }
+      BF8 ub[2];
+      split(f, ub);
+      split(g, wu[c]);
+      BF8 P[4][2];
+#pragma unroll
+      for (int i = 2 * c; i < 4; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          P[i][y] = *(const BF8*)&b.prep[kGate + kTri + (2 * piece(i, c) + y) * 256 + lane * 4];
+#pragma unroll
+      for (int y = 0; y < 3; ++y)
+#pragma unroll
+        for (int i = 2 * c; i < 4; ++i) O[i] = mfma(P[i][y == 1], ub[y == 2], O[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const __bf16 y = (__bf16)O[i][r];
+        so[wave][(16 * i + 4 * q4 + r) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+      }
+    // ---- the state
+    const float eall = b.prep[192];
+#pragma unroll
+    for (int t4 = 0; t4 < 2 * kKS; t4 += 4) {
+#pragma unroll
+      for (int y = t4; y < t4 + 4; ++y)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[y][r] *= eall;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        BF8 kt[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint16_t* p =
+              &b.k[at<DK>(32 * c + 4 * q4 + (m >> 2), 32 * ((t4 + y) >> 1) + 8 * (m & 3) + 4 * (y & 1))];
+          kt[y] = join(read_tr(p), read_tr(p + 16 * DK));
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) S[t4 + y] = mfma(kt[y], wu[c][p], S[t4 + y]);
+      }
+    }
+  };
+
+  int t = start;
+  auto step = [&](auto& b, auto& other) {
+    const int next = min((t / kL + 1) * kL, end);
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0: what this wave brings is in LDS
+    __syncthreads();                         // this chunk is in LDS, and the one before has been read
+    if constexpr (kTwo)
+      if (next < end) fetch(other, next, min(next + kL, end));
+    put_out();
+    work(b, t, next - t);
+    done_t = t;
+    done_n = next - t;
+    if constexpr (!kTwo) {
+      __syncthreads();
+      if (next < end) fetch(b, next, min(next + kL, end));
+    }
     t = next;
+  };
+  if (start < end) fetch(buf0, start, min((start / kL + 1) * kL, end));
+  while (t < end) {
+    if constexpr (kTwo) {
+      step(buf0, buf1);
+      if (t < end) step(buf1, buf0);
+    } else {
+      step(buf0, buf0);
+    }
   }
+  put_out();
   if (v < a.dv)
 #pragma unroll
-    for (int t = 0; t < 2 * kKS; ++t)
-      *(F4*)(a.final + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1)) = S[t];
+    for (int y = 0; y < 2 * kKS; ++y)
+      *(F4*)(a.final + (st + head + v) * DK + 32 * (y >> 1) + 8 * q4 + 4 * (y & 1)) = S[y];
 }
 
 template <int DK, bool VEC>
 hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  constexpr int WAVES = 4;
+  constexpr int WAVES = 2;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
   k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
   k_delta_scan<DK, WAVES, VEC><<<dim3((uint32_t)(a.n * a.H * vchunks)), 64 * WAVES, 0, s>>>(a, g.states, vchunks);

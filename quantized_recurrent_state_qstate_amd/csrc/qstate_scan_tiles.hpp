@@ -117,6 +117,16 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
   return r;
 }
 
+// 16 bytes a lane from a buffer at `offset` to LDS, lane after lane from `to` on
+// (the same in all lanes); beyond the buffer's bound they are zeros.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint16_t* to, int offset) {
+  typedef __attribute__((address_space(3))) void* L;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (L)to, 16, offset, 0, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ int flip(int r);
+
 // 64 rows of a bf16 tensor from row t0's element `p` on, `n` of them real: 16-byte
 // pieces of `width` elements, zeros behind the last row.  VEC: buffer loads,
 // whose bound is the last real row's end (rows are at most 2^24 elements
@@ -146,6 +156,13 @@ struct Tile {
       return (U4){d[0], d[1], d[2], d[3]};
     }
   }
+  // Elements e .. e + 511 of an LDS tile with rows of N, as at<N>() lays them, by one wave.
+  template <int N>
+  __device__ __forceinline__ void bring(uint16_t* tile, int e, int lane) const {
+    const int r = (e + lane * 8) / N, c = (((lane * 8) % N / 8) ^ flip<N>(r)) * 8;
+    if constexpr (VEC) to_lds(rsrc, tile + e, (r * stride + c) * 2);
+    else *(U4*)(tile + e + lane * 8) = load(r, c);
+  }
 };
 
 // The largest exponents (as 15-bit patterns without sign) of 8 bf16 numbers, by halves.
@@ -157,23 +174,35 @@ __device__ __forceinline__ H2 largest(H2 x, U4 u) {
 }
 __device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
 
+// Element (r, c) of an LDS tile with rows of N elements.  The 16-byte pieces of
+// a row are exchanged by the row's low bits, so that both ways of reading, 8
+// channels of 16 rows and (transposed) 4 rows of 4 x 4 channels, meet every
+// bank once.  Rows of 32 elements need no exchange.
+template <int N>
+__device__ __forceinline__ int flip(int r) {
+  return N >= 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : N == 64 ? ((r & 3) << 1) | ((r >> 2) & 1) : 0;
+}
+template <int N>
+__device__ __forceinline__ int at(int r, int c) {
+  return r * N + (((c >> 3) ^ flip<N>(r)) << 3) + (c & 7);
+}
+
 // A chunk token by token, for one with a value that is not finite: in the
 // products of a whole chunk a zero times such a value would reach the tokens
 // before it.  The state tiles are those of the scans (lane m, q4: column m,
-// channels 32 i + 8 q4 .. + 7); k, q and v lie in LDS with rows of KR and VR
-// elements, and the outputs take v's place.
-template <int DK, bool DELTA, int KR, int VR>
-__device__ __forceinline__ void by_token(const ScanArgs& a, int t, int n, int h, const uint16_t* sk, const uint16_t* sq,
-                                         uint16_t* sv, int col, F4 (&S)[DK / 16]) {
+// channels 32 i + 8 q4 .. + 7); K(i, c) and Q(i, c) give 8 channels from c on
+// of token i, V(i) the lane's v, and O(i, o) takes the output.
+template <int DK, bool DELTA, class FK, class FQ, class FV, class FO>
+__device__ __forceinline__ void by_token(const ScanArgs& a, int t, int n, int h, FK K, FQ Q, FV V, FO O, F4 (&S)[DK / 16]) {
   const int lane = (int)threadIdx.x & 63, q4 = lane >> 4;
   const float skip = a.skip ? a.skip[h] : 0.0f;
   for (int i = 0; i < n; ++i) {
     const float d = a.decay[(int64_t)(t + i) * a.ds + h], beta = a.beta ? a.beta[(int64_t)(t + i) * a.bs + h] : 1.0f;
-    const float v = __uint_as_float((uint32_t)sv[i * VR + col] << 16);
+    const float v = V(i);
     float w = 0.0f, o = 0.0f;
 #pragma unroll
     for (int c = 0; c < DK / 32; ++c) {
-      const BF8 k = *(const BF8*)&sk[i * KR + 32 * c + 8 * q4];
+      const BF8 k = K(i, 32 * c + 8 * q4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = S[2 * c + (j >> 2)][j & 3] * d;
@@ -188,7 +217,7 @@ __device__ __forceinline__ void by_token(const ScanArgs& a, int t, int n, int h,
     const float u = beta * (v - w);
 #pragma unroll
     for (int c = 0; c < DK / 32; ++c) {
-      const BF8 k = *(const BF8*)&sk[i * KR + 32 * c + 8 * q4], q = *(const BF8*)&sq[i * KR + 32 * c + 8 * q4];
+      const BF8 k = K(i, 32 * c + 8 * q4), q = Q(i, 32 * c + 8 * q4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = fmaf(u, (float)k[j], S[2 * c + (j >> 2)][j & 3]);
@@ -199,8 +228,7 @@ __device__ __forceinline__ void by_token(const ScanArgs& a, int t, int n, int h,
     o += __shfl_xor(o, 16);
     o += __shfl_xor(o, 32);
     if (a.skip) o = fmaf(skip, v, o);
-    const __bf16 y = (__bf16)o;
-    if (q4 == 0) sv[i * VR + col] = __builtin_bit_cast(uint16_t, y);
+    if (q4 == 0) O(i, o);
   }
 }
 
