@@ -30,12 +30,15 @@ namespace {
 
 // What the first launch leaves for a chunk of a head.
 constexpr int kGate = 256;                    // floats: 2^{c_i}, 2^{c_last - c_i}, beta_i, 2^{c_last}, oddness
-constexpr int kTri = 10 * 256;                // floats: T's lower tiles, a float4 a lane
-constexpr int kPieces = 6 * 2 * 64 * 8;       // bf16: P's lower 16 x 32 tiles, upper and lower halves, 8 a lane
-constexpr int kPrepFloats = kGate + kTri + kPieces / 2;
+constexpr int kTile = 64 * 8 / 2;             // floats of a 16 x 32 tile in bf16, 8 elements a lane
+constexpr int kTri = 6 * 3 * kTile;           // T's lower tiles in three pieces
+constexpr int kPairs = 6 * 2 * kTile;         // P's lower tiles in two
+constexpr int kPrepFloats = kGate + kTri + kPairs;
 static_assert(kPrepFloats * 4 == kScanPrepBytes, "workspace a chunk and head");
 
-__device__ __forceinline__ int tri(int b, int a) { return b * (b + 1) / 2 + a; }
+// The lower 16 x 32 tiles of a 64 x 64 matrix: rows 16 i .., columns 32 c ...
+// A lane (m, q4) has row m's columns 4 q4 .. + 3 and 16 + 4 q4 .. + 3: the
+// order in which accumulators of 16 x 16 tiles are the other operand.
 __device__ __forceinline__ int piece(int i, int c) { return i < 2 ? i : 2 * i - 2 + c; }
 
 template <int DK, bool VEC>
@@ -173,12 +176,15 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
 #pragma unroll
       for (int r = 0; r < 4; ++r) sa[(16 * b + 4 * q4 + r) * kAR + 16 * wave + m] = X[b][r];
   __syncthreads();
+  for (int c = 0; c <= wave >> 1; ++c) {
+    const F4 x = *(const F4*)&sa[(16 * wave + m) * kAR + 32 * c + 4 * q4];
+    const F4 y = *(const F4*)&sa[(16 * wave + m) * kAR + 32 * c + 16 + 4 * q4];
+    const float f[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    BF8 t[3];
+    split(f, t);
 #pragma unroll
-  for (int b = 0; b < 4; ++b)
-#pragma unroll
-    for (int x = 0; x <= b; ++x)
-      if (tri(b, x) % 4 == wave)
-        *((F4*)(out + kGate) + tri(b, x) * 64 + lane) = *(const F4*)&sa[(16 * b + m) * kAR + 16 * x + 4 * q4];
+    for (int p = 0; p < 3; ++p) *(BF8*)(out + kGate + (3 * piece(wave, c) + p) * kTile + lane * 4) = t[p];
+  }
 }
 
 // A chunk of a workgroup's columns in LDS.
@@ -220,27 +226,24 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       S[t] = *(const F4*)(a.initial + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
   }
 
-  // The chunk from token t to t1 on its way into b.
-  auto fetch = [&](Buf& b, int t, int t1) {
+  // The next chunk's pieces of 1 KB, `kPieces` for each wave, brought one by one.
+  constexpr int kK = kL * DK / 512 / WAVES, kV = kL * kDV / 512 / WAVES, kP = (kPrepFloats / 256 + WAVES - 1) / WAVES;
+  constexpr int kPieces = 2 * kK + kV + kP;
+  auto bringing = [&](Buf& b, int t, int t1) {   // piece i of the chunk from t to t1 into b
     const int rows = t1 - t;
-    const Tile<VEC> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
-    const Tile<VEC> tq(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK);
-    const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
-    const float* p = prep + ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats;
-#pragma unroll
-    for (int i = 0; i < kL * DK / 512 / WAVES; ++i) {
-      const int e = (i * WAVES + wave) * 512;                       // the wave's 1 KB piece of the tile
-      tk.template bring<DK>(b.k, e, lane);
-      tq.template bring<DK>(b.q, e, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < kL * kDV / 512 / WAVES; ++i) tv.template bring<kDV>(b.v, (i * WAVES + wave) * 512, lane);
-    const Tile<true> tp(p, 0, 0, 1, kPrepFloats * 2);
-#pragma unroll
-    for (int i = 0; i < (kPrepFloats / 256 + WAVES - 1) / WAVES; ++i) {
-      const int e = i * WAVES + wave;
-      if (e < kPrepFloats / 256) to_lds(tp.rsrc, (uint16_t*)b.prep + e * 512, e * 1024 + lane * 16);
-    }
+    return [&b, wave, lane, tk = Tile<VEC>(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK),
+            tq = Tile<VEC>(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK),
+            tv = Tile<VEC>(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0)),
+            tp = Tile<true>(prep, 2 * ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats, 0, min(rows, 1), kPrepFloats * 2)](
+               int i) {
+      if (i < kK) tk.template bring<DK>(b.k, (i * WAVES + wave) * 512, lane);
+      else if (i < 2 * kK) tq.template bring<DK>(b.q, ((i - kK) * WAVES + wave) * 512, lane);
+      else if (i < 2 * kK + kV) tv.template bring<kDV>(b.v, ((i - 2 * kK) * WAVES + wave) * 512, lane);
+      else if (i < kPieces) {
+        const int e = (i - 2 * kK - kV) * WAVES + wave;
+        if (e < kPrepFloats / 256) to_lds(tp.rsrc, (uint16_t*)b.prep + e * 512, e * 1024 + lane * 16);
+      }
+    };
   };
 
   int done_t = 0, done_n = 0;                // the chunk whose outputs wait in `so`
@@ -262,7 +265,15 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     }
   };
 
-  auto work = [&](Buf& b, int t, int n) {
+  // A chunk; the next one's pieces are asked for on the way, a few at each of
+  // kPoints places: asked for at once they would hold the wave up.
+  constexpr int kPoints = kKS + 6, kEach = (kPieces + kPoints - 1) / kPoints;
+  auto work = [&](Buf& b, auto& bring, int t, int n) {
+    auto point = [&](int i) {
+      if constexpr (kTwo)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) bring(i * kEach + j);
+    };
     // ---- v of the wave's columns; a value that is not finite
     BF4 x[4];
     H2 most = (H2){0, 0};
@@ -273,6 +284,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       most = largest(most, (U4){u.x, u.y, 0, 0});
     }
     if (b.prep[193] != 0.0f || __ballot(odd(most)) != 0) {
+      if constexpr (kTwo)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) bring(i);
       by_token<DK, true>(
           a, t, n, h, [&](int i, int c) { return *(const BF8*)&b.k[at<DK>(i, c)]; },
           [&](int i, int c) { return *(const BF8*)&b.q[at<DK>(i, c)]; },
@@ -288,56 +302,90 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     F4 O[4], R[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) O[i] = R[i] = (F4){0, 0, 0, 0};
+    BF8 qf[2][4], kf[2][4];
+    auto rows = [&](int c) {
 #pragma unroll
-    for (int c = 0; c < kKS; ++c) {
-      BF8 sp[3];
+      for (int i = 0; i < 4; ++i) {
+        kf[c & 1][i] = *(const BF8*)&b.k[at<DK>(16 * i + m, 32 * c + 8 * q4)];
+        qf[c & 1][i] = *(const BF8*)&b.q[at<DK>(16 * i + m, 32 * c + 8 * q4)];
+      }
+    };
+    BF8 sp[2][3];
+    auto pieces = [&](int c) {
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = S[2 * c + (j >> 2)][j & 3];
-      split(f, sp);
-      BF8 qf[4], kf[4];
+      split(f, sp[c & 1]);
+    };
+    rows(0);
+    pieces(0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kf[i] = *(const BF8*)&b.k[at<DK>(16 * i + m, 32 * c + 8 * q4)];
-        qf[i] = *(const BF8*)&b.q[at<DK>(16 * i + m, 32 * c + 8 * q4)];
-      }
+    for (int c = 0; c < kKS; ++c) {
+      if (c + 1 < kKS) rows(c + 1);
+      point(c);
       // products on one accumulator are kept apart: each takes several issue slots
 #pragma unroll
       for (int y = 0; y < 3; ++y)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          R[i] = mfma(kf[i], sp[y], R[i]);
-          if (y < 2) O[i] = mfma(qf[i], sp[y], O[i]);
+          R[i] = mfma(kf[c & 1][i], sp[c & 1][y], R[i]);
+          if (y < 2) O[i] = mfma(qf[c & 1][i], sp[c & 1][y], O[i]);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const F4 e = *(const F4*)&b.prep[16 * i + 4 * q4], bt = *(const F4*)&b.prep[128 + 16 * i + 4 * q4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        R[i][r] = bt[r] * fmaf(-e[r], R[i][r], (float)x[i][r]);
-        O[i][r] *= e[r];
-        if (a.skip) O[i][r] = fmaf(skip, (float)x[i][r], O[i][r]);
-      }
+      if (c + 1 < kKS) pieces(c + 1);
     }
     // ---- U = T R
     F4 U[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) U[i] = (F4){0, 0, 0, 0};
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      F4 T[4];
+    for (int c = 0; c < 2; ++c) {
+      BF8 T[4][3];
 #pragma unroll
-      for (int i = y; i < 4; ++i) T[i] = *(const F4*)&b.prep[kGate + tri(i, y) * 256 + lane * 4];
+      for (int i = 2 * c; i < 4; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int p = 0; p < 3; ++p) T[i][p] = *(const BF8*)&b.prep[kGate + (3 * piece(i, c) + p) * kTile + lane * 4];
+      float f[8];
 #pragma unroll
-        for (int i = y; i < 4; ++i) U[i] = mfma1(T[i][r], R[y][r], U[i]);
+      for (int y = 0; y < 2; ++y) {
+        const int i = 2 * c + y;
+        const F4 e = *(const F4*)&b.prep[16 * i + 4 * q4], bt = *(const F4*)&b.prep[128 + 16 * i + 4 * q4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[4 * y + r] = bt[r] * fmaf(-e[r], R[i][r], (float)x[i][r]);
+          O[i][r] *= e[r];
+          if (a.skip) O[i][r] = fmaf(skip, (float)x[i][r], O[i][r]);
+        }
+      }
+      BF8 rp[3];
+      split(f, rp);
+      point(kKS + c);
+      // the six products of pieces that reach 24 bits
+#pragma unroll
+      for (int p = 0; p < 6; ++p)
+#pragma unroll
+        for (int i = 2 * c; i < 4; ++i)
+          U[i] = mfma(T[i][p == 2 || p == 3 ? 1 : p == 5 ? 2 : 0], rp[p == 1 || p == 3 ? 1 : p == 4 ? 2 : 0], U[i]);
     }
     // ---- outputs: P u on top
-    BF8 wu[2][3];
+    BF8 wu[2][3], kt[2][4];
+    auto columns = [&](int z) {              // k transposed: tokens 32 (z & 1) .., tiles 4 (z >> 1) ..
+      const int c = z & 1, t4 = 4 * (z >> 1);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint16_t* p =
+            &b.k[at<DK>(32 * c + 4 * q4 + (m >> 2), 32 * ((t4 + y) >> 1) + 8 * (m & 3) + 4 * (y & 1))];
+        kt[z & 1][y] = join(read_tr(p), read_tr(p + 16 * DK));
+      }
+    };
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      BF8 P[4][2];
+#pragma unroll
+      for (int i = 2 * c; i < 4; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          P[i][y] = *(const BF8*)&b.prep[kGate + kTri + (2 * piece(i, c) + y) * kTile + lane * 4];
+      if (c == 1) columns(0);
       float f[8], g[8];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -350,47 +398,37 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       }
       BF8 ub[2];
       split(f, ub);
-      split(g, wu[c]);
-      BF8 P[4][2];
-#pragma unroll
-      for (int i = 2 * c; i < 4; ++i)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          P[i][y] = *(const BF8*)&b.prep[kGate + kTri + (2 * piece(i, c) + y) * 256 + lane * 4];
+      point(kKS + 2 + c);
 #pragma unroll
       for (int y = 0; y < 3; ++y)
 #pragma unroll
         for (int i = 2 * c; i < 4; ++i) O[i] = mfma(P[i][y == 1], ub[y == 2], O[i]);
+      split(g, wu[c]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const __bf16 y = (__bf16)O[i][r];
-        so[wave][(16 * i + 4 * q4 + r) * 16 + m] = __builtin_bit_cast(uint16_t, y);
-      }
     // ---- the state
     const float eall = b.prep[192];
 #pragma unroll
-    for (int t4 = 0; t4 < 2 * kKS; t4 += 4) {
+    for (int z = 0; z < kKS; ++z) {
+      const int c = z & 1, t4 = 4 * (z >> 1);
+      if (z + 1 < kKS) columns(z + 1);
+      if (c == 0)
 #pragma unroll
-      for (int y = t4; y < t4 + 4; ++y)
+        for (int y = t4; y < t4 + 4; ++y)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[y][r] *= eall;
+          for (int r = 0; r < 4; ++r) S[y][r] *= eall;
+      if (z < 2) point(kKS + 4 + z);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        BF8 kt[4];
+      for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint16_t* p =
-              &b.k[at<DK>(32 * c + 4 * q4 + (m >> 2), 32 * ((t4 + y) >> 1) + 8 * (m & 3) + 4 * (y & 1))];
-          kt[y] = join(read_tr(p), read_tr(p + 16 * DK));
-        }
+        for (int y = 0; y < 4; ++y) S[t4 + y] = mfma(kt[z & 1][y], wu[c][p], S[t4 + y]);
+      if (z < 2)                             // the outputs, behind the products that made them
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+        for (int i = 2 * z; i < 2 * z + 2; ++i)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) S[t4 + y] = mfma(kt[y], wu[c][p], S[t4 + y]);
-      }
+          for (int r = 0; r < 4; ++r) {
+            const __bf16 y = (__bf16)O[i][r];
+            so[wave][(16 * i + 4 * q4 + r) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+          }
     }
   };
 
@@ -399,19 +437,24 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     const int next = min((t / kL + 1) * kL, end);
     __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0: what this wave brings is in LDS
     __syncthreads();                         // this chunk is in LDS, and the one before has been read
-    if constexpr (kTwo)
-      if (next < end) fetch(other, next, min(next + kL, end));
+    // behind the last chunk this is an empty one: the other buffer gets zeros
+    const auto bring = bringing(other, next, min(next + kL, end));
     put_out();
-    work(b, t, next - t);
+    work(b, bring, t, next - t);
     done_t = t;
     done_n = next - t;
     if constexpr (!kTwo) {
       __syncthreads();
-      if (next < end) fetch(b, next, min(next + kL, end));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) bring(i);
     }
     t = next;
   };
-  if (start < end) fetch(buf0, start, min((start / kL + 1) * kL, end));
+  if (start < end) {
+    const auto bring = bringing(buf0, start, min((start / kL + 1) * kL, end));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) bring(i);
+  }
   while (t < end) {
     if constexpr (kTwo) {
       step(buf0, buf1);

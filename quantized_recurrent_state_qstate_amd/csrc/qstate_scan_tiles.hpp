@@ -137,6 +137,7 @@ struct Tile {
   const uint16_t* p;
   __amdgpu_buffer_rsrc_t rsrc;
   int32_t stride, n, width;
+  Tile() = default;
   __device__ __forceinline__ Tile(const void* base, int64_t at, int64_t row, int n_, int width_)
       : p((const uint16_t*)base + at), stride((int32_t)row), n(n_), width(width_) {
     if constexpr (VEC)
