@@ -9,7 +9,7 @@ Translation units:
                              compile in parallel
   qstate_misc.hip            quantize / dequantize / fill kernels, dispatch
   qstate_conv.hip, qstate_qk.hip, qstate_slots.hip, qstate_scan.hip, qstate_scan_chunk.hip,
-  qstate_scan_delta.hip
+  qstate_scan_delta.hip, qstate_scan_key.hip
                              the operators around the step: convolution, q/k
                              norm and rotation, slot copies, prompt scan
   qstate_ops_host.cpp        their C ABI: argument checks, launches
@@ -74,7 +74,8 @@ def units():
             obj = os.path.join(OBJ, f"qstate_step_{fam}_q{qb}_{RND_NAME[rnd]}.o")
             out.append((src, [f"-DQS_QB={qb}", f"-DQS_RND={rnd}"], obj))
     for name in ("qstate_misc.hip", "qstate_conv.hip", "qstate_qk.hip", "qstate_slots.hip", "qstate_scan.hip",
-                 "qstate_scan_chunk.hip", "qstate_scan_delta.hip", "qstate_host.cpp", "qstate_ops_host.cpp"):
+                 "qstate_scan_chunk.hip", "qstate_scan_delta.hip",
+                 "qstate_scan_key.hip", "qstate_host.cpp", "qstate_ops_host.cpp"):
         out.append((os.path.join(CSRC, name), [], os.path.join(OBJ, name + ".o")))
     return out
 

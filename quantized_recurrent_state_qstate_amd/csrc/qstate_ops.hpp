@@ -100,9 +100,11 @@ hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 struct ScanSegs {
   int32_t seg, count;
   float* states;           // [count][H][dv][dk], null: no sequence is cut; delta rule: [count][H] kScanPrepBytes
-  float* total;            // [count][H] log2 of a segment's whole decay
+  float* total;            // [count][H] or [count][H][dk]: a segment's whole decay
 };
 constexpr int kScanPrepBytes = 1024 + 18 * 1024 + 12 * 1024;
+hipError_t launch_scan_key(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
+hipError_t launch_scan_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 

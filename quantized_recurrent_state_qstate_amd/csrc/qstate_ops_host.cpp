@@ -91,7 +91,7 @@ qs_status check_conv(const qstate_conv* c, bool step, qs::ConvArgs* a) {
            c->x_stride % v == 0 && c->out_stride % v == 0;
   // workgroups of the narrowest variant
   const int64_t tiles = (C + 63) / 64;
-  const int64_t blocks = tiles * (step ? rows : rows / 64 + 1 + c->n);
+  const int64_t blocks = tiles * (step ? rows : rows / 16 + 1 + c->n);
   if (blocks > 0x7FFFFFFF) return op_fail(QS_EUNSUPPORTED, "%lld rows of %lld channels in one call", (long long)rows, (long long)C);
   return QS_OK;
 }
@@ -210,8 +210,8 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
   return QS_OK;
 }
 
-// How a scan runs.  The chunked kernels take bf16 prompts with one decay a
-// head; everything else runs token by token.  Additive sequences are cut into
+// How a scan runs.  The chunked kernels take bf16 prompts but the delta rule
+// with a decay for every key channel; everything else runs token by token.  Additive sequences are cut into
 // segments when the heads alone would leave compute units idle: about 512
 // workgroups, no segment shorter than 256 tokens (each costs a state written
 // and read).
@@ -222,7 +222,7 @@ struct ScanPlan {
 };
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
-  p.chunked = a.bf16 && !a.key && a.T >= 64;
+  p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= 64;
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
   if (!p.chunked) return p;
@@ -238,7 +238,7 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   p.segs.seg = (int32_t)seg;
   p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);
   p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)a.dv * (uint64_t)a.dk * 4u;
-  p.total = ((uint64_t)p.segs.count * (uint64_t)a.H * 4u + 255u) / 256u * 256u;
+  p.total = ((uint64_t)p.segs.count * (uint64_t)a.H * (a.key ? (uint64_t)a.dk : 1u) * 4u + 255u) / 256u * 256u;
   return p;
 }
 
@@ -321,7 +321,8 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
           a.dv % v == 0 && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0 && c->v_stride % v == 0 &&
                                        c->out_stride % v == 0));
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
-  hipError_t e = p.chunked ? (a.delta ? qs::launch_scan_delta : qs::launch_scan_chunk)(a, p.segs, reinterpret_cast<hipStream_t>(stream))
+  hipError_t e = p.chunked ? (a.delta ? qs::launch_scan_delta : a.key ? qs::launch_scan_key : qs::launch_scan_chunk)(
+                                 a, p.segs, reinterpret_cast<hipStream_t>(stream))
                            : qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));
   return op_ok();

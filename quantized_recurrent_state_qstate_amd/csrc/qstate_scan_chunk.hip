@@ -364,10 +364,10 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           *(F4*)(to + (head + col) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1)) = S[v][t];
     }
   }
-  if (!OUT && tid == 0 && v0 == 0) g.total[(int64_t)s * a.H + h] = (float)total;
+  if (!OUT && tid == 0 && v0 == 0) g.total[(int64_t)s * a.H + h] = __builtin_amdgcn_exp2f((float)total);
 }
 
-// States between segments: for each sequence, S = initial, then S = 2^total S + local
+// States between segments: for each sequence, S = initial, then S = decay S + local
 // from segment to segment; segment s's place takes the state before it.
 __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanSegs g, int blocks) {
   const int seq = (int)blockIdx.x / blocks;
@@ -385,11 +385,17 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
   F4 L = (F4){0, 0, 0, 0};
   if (c0 < c1) L = st[(int64_t)(c0 + seq) * all + e];
   for (int c = c0; c < c1; ++c) {
-    const float d = __builtin_amdgcn_exp2f(g.total[(int64_t)(c + seq) * a.H + h]);
+    F4 d;
+    if (a.key) {
+      d = *(const F4*)&g.total[((int64_t)(c + seq) * a.H + h) * a.dk + e * 4 % a.dk];
+    } else {
+      const float x = g.total[(int64_t)(c + seq) * a.H + h];
+      d = (F4){x, x, x, x};
+    }
     F4 next = (F4){0, 0, 0, 0};
     if (c + 1 < c1) next = st[(int64_t)(c + 1 + seq) * all + e];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) S[r] = fmaf(d, S[r], L[r]);
+    for (int r = 0; r < 4; ++r) S[r] = fmaf(d[r], S[r], L[r]);
     st[(int64_t)(c + 1 + seq) * all + e] = S;
     L = next;
   }
@@ -401,8 +407,8 @@ hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
   if (g.states) {
     k_scan_chunk<DK, NV, WAVES, false, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
-    const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
-    k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
+    const hipError_t e = launch_scan_join(a, g, s);
+    if (e != hipSuccess) return e;
   }
   k_scan_chunk<DK, NV, WAVES, true, VEC><<<dim3(grid), 64 * WAVES, 0, s>>>(a, g, vchunks);
   return hipGetLastError();
@@ -414,6 +420,12 @@ hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_scan_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
+  k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
+  return hipGetLastError();
+}
 
 hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   return a.dk == 64 ? chunk_dk<64>(a, g, s) : a.dk == 128 ? chunk_dk<128>(a, g, s) : chunk_dk<256>(a, g, s);
