@@ -211,10 +211,16 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
 }
 
 // How a scan runs.  The chunked kernels take bf16 prompts but the delta rule
-// with a decay for every key channel; everything else runs token by token.  Additive sequences are cut into
-// segments when the heads alone would leave compute units idle: about 512
-// workgroups, no segment shorter than 256 tokens (each costs a state written
-// and read).
+// with a decay for every key channel, if the sequences are long enough on the
+// average: one sequence of 16 tokens, 32 heads of 128 x 128, takes 7.4 us
+// against 8.1 token by token (one of 8: 7.4, 6.1), sixteen of 64 by the delta
+// rule 71 against 90 us (of 32: 68, 50).  Everything else runs token by token.
+// Additive sequences are cut into segments when the heads alone would leave
+// compute units idle; a segment costs a state written, read and written again,
+// so it has at least 256 tokens (one decay a head; 16384 tokens of 32 heads of
+// 128 x 64: 140 us with segments for 512 workgroups, 155 us for 1024, 175 us
+// for 384) or 128 (a decay a channel, whose blocks are slower; 2048 tokens of
+// 32 heads of 128 x 128: 118 us for 1024, 164 us with at least 256 tokens).
 struct ScanPlan {
   bool chunked;
   qs::ScanSegs segs;
@@ -222,7 +228,9 @@ struct ScanPlan {
 };
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
-  p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= 64;
+  // sequences' average length: below 16 tokens (delta rule: 48, for its first
+  // launch) the token by token kernel is ahead
+  p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= (int64_t)a.n * (a.delta ? 48 : 16);
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
   if (!p.chunked) return p;
@@ -233,7 +241,7 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     return p;
   }
   const int64_t work = (int64_t)a.T * a.H * ((a.dv + 63) / 64);
-  const int64_t seg = std::max<int64_t>(256, (work / 512 + 63) / 64 * 64);
+  const int64_t seg = std::max<int64_t>(a.key ? 128 : 256, (work / (a.key ? 1024 : 512) + 63) / 64 * 64);
   if (seg >= a.T) return p;
   p.segs.seg = (int32_t)seg;
   p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);

@@ -472,7 +472,10 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 
 template <int DK, bool VEC>
 hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  constexpr int WAVES = 2;
+  // 64 columns a workgroup: with 32, twice as many workgroups bring the same
+  // keys (one sequence of 7868 tokens, 32 heads of 128 x 128: 493 against 506 us
+  // in all; sixteen of 256: 107, 172).
+  constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
   k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
   k_delta_scan<DK, WAVES, VEC><<<dim3((uint32_t)(a.n * a.H * vchunks)), 64 * WAVES, 0, s>>>(a, g.states, vchunks);
