@@ -344,7 +344,11 @@ qs_status qstate_qk_norm_rotate(const qstate_qk* a, void* stream);
  *   h*k_heads/H .. share a query and key head (k_heads divides H).
  *   out = S q (+ skip[h] v); final = the state after the last token (what
  *   qstate_quantize takes), or `initial` for a sequence of no tokens.
- * decay must not be negative. */
+ * decay must not be negative.  A decay of 0 forgets everything before its
+ * token.  A value that is not finite reaches only its own token and later ones
+ * of its sequence.  With bf16 inputs products take operands in bf16 pieces, two
+ * for out (which is bf16) and three for the state; sums are fp32.  q, k and v
+ * strides of up to 2^24 elements. */
 typedef struct {
   const void* q;
   const void* k;
@@ -385,7 +389,8 @@ typedef struct {
  * and hands states from one pool to another in one launch.  Elements with a
  * slot out of range are skipped.  Destinations must be distinct, and within
  * one pool no destination may be another element's source (such elements
- * race).  extra: up to 6 more buffers of both pools.
+ * race).  extra: up to 6 more buffers of both pools.  Stochastic rounding draws
+ * by slot: forks of one state round differently from then on.
  * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
 qs_status qstate_copy_slots(qstate_handle* h, const qstate_tensors* pool, const qstate_tensors* source,
                             int32_t src_slots, int32_t n, const int32_t* src_slot, const int32_t* dst_slot,

@@ -98,7 +98,19 @@ __global__ __launch_bounds__(256) void k_qk(const QkArgs a, int splits, int per)
       for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
 #pragma unroll
       for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
-      const float inv = 1.0f / sqrtf((a.norm == 2 ? ss / (float)a.dim : ss) + a.eps);
+      float inv = 1.0f / sqrtf((a.norm == 2 ? ss / (float)a.dim : ss) + a.eps);
+      if (__ballot(ss > 0x1p126f)) {       // squares beyond fp32: again with x 2^-70, where eps is nothing
+        float s2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s2 = fmaf(f[j] * 0x1p-70f, f[j] * 0x1p-70f, s2);
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) s2 += __shfl_xor(s2, m);
+        if (ss > 0x1p126f) {
+          inv = 1.0f / sqrtf(a.norm == 2 ? s2 / (float)a.dim : s2);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= 0x1p-70f;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= inv;
       const float* w = a.w[s];

@@ -144,3 +144,20 @@ def test_binding_checks():
             qk_norm_rotate(*args, **kw)
     assert check_rows("x", torch.zeros(4, 10)[:, 2:6], torch.float32, (4, 4), torch.device("cpu")) == 10
     assert check_rows("x", torch.zeros(1, 10)[:, 2:6], torch.float32, (1, 4), torch.device("cpu")) == 4
+
+
+def test_handle_calls_host_code_under_sanitizers(tmp_path):
+    """The scan's, copy's and compaction's argument checks, plans and workspaces, with stand-ins for HIP."""
+    import os
+    import shutil
+
+    from test_sanitizers import HERE, ROOT, SAN, _run
+    gxx, inc = shutil.which("g++"), "/opt/rocm/include"
+    if not gxx or not os.path.exists(os.path.join(inc, "hip", "hip_runtime_api.h")):
+        pytest.skip("g++ or the HIP headers not available")
+    csrc = os.path.join(ROOT, "quantized_recurrent_state_qstate_amd", "csrc")
+    exe = str(tmp_path / "ops_driver")
+    out = _run([gxx, "-std=c++17", *SAN, "-D__HIP_PLATFORM_AMD__", "-I", inc, "-I", os.path.join(ROOT, "include"),
+                "-I", csrc, os.path.join(csrc, "qstate_host.cpp"), os.path.join(csrc, "qstate_ops_host.cpp"),
+                os.path.join(HERE, "ops_driver.cpp"), "-o", exe], exe)
+    assert "0 failed checks" in out, out
