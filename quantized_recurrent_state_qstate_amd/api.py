@@ -158,17 +158,22 @@ def check_rows(name: str, t, dtype, shape, device) -> int:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != width:
-            raise ValueError(f"{name}: rows are not contiguous")
-        width *= size
+    st = t.stride()
+    if len(st) == 3 and st[2] == 1 and st[1] == shape[2]:
+        width = shape[1] * shape[2]
+    else:
+        width = 1
+        for size, stride in zip(reversed(shape[1:]), reversed(st[1:])):
+            if size != 1 and stride != width:
+                raise ValueError(f"{name}: rows are not contiguous")
+            width *= size
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    stride = t.stride(0)
-    if t.shape[0] > 1 and stride < width:
-        raise ValueError(f"{name}: rows overlap (stride {stride} of {width})")
-    return stride if t.shape[0] > 1 else width
+    if shape[0] <= 1:
+        return width
+    if st[0] < width:
+        raise ValueError(f"{name}: rows overlap (stride {st[0]} of {width})")
+    return st[0]
 
 
 def _empty(shape, dtype, device, stream):
@@ -202,6 +207,7 @@ class QState:
                    "qstate_init")
         self.sizes = {n: int(getattr(s, n)) for n, _ in _lib.Sizes._fields_}
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._scan_bytes = {}     # workspace sizes by (tokens, sequences, key heads)
 
     def close(self) -> None:
         if self._h:
@@ -351,12 +357,16 @@ class QState:
         a = _lib.Scan(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(beta), _ptr(skip),
                       _ptr(initial), final.data_ptr(), out.data_ptr(), _ptr(offsets), qs, ks, vs, ds, bs, os, T, n, G)
         L = _lib.lib()
-        need = ctypes.c_uint64()
-        _lib.check(L.qstate_scan_workspace(self._h, ctypes.byref(a), ctypes.byref(need)), "qstate_scan_workspace")
+        need = self._scan_bytes.get((T, n, G))
+        if need is None:
+            z = ctypes.c_uint64()
+            _lib.check(L.qstate_scan_workspace(self._h, ctypes.byref(a), ctypes.byref(z)), "qstate_scan_workspace")
+            if len(self._scan_bytes) >= 4096:
+                self._scan_bytes.clear()
+            need = self._scan_bytes[T, n, G] = z.value
         # the call's own: a captured call keeps it in its graph's memory
-        ws = _empty((need.value,), torch.uint8, dev, stream) if need.value else None
-        _lib.check(L.qstate_scan(self._h, ctypes.byref(a), _ptr(ws), need.value, raw_stream(stream, dev)),
-                   "qstate_scan")
+        ws = _empty((need,), torch.uint8, dev, stream) if need else None
+        _lib.check(L.qstate_scan(self._h, ctypes.byref(a), _ptr(ws), need, raw_stream(stream, dev)), "qstate_scan")
         return out, final
 
     def _checked(self, st: dict, slots: int) -> _lib.Tensors:
