@@ -43,7 +43,10 @@ struct Vec {
   };
 };
 
-__device__ __forceinline__ float silu(float y) { return y * __builtin_amdgcn_rcpf(1.0f + __expf(-y)); }
+// The bare 2^x: a subnormal e^-y would vanish in the sum anyway.
+__device__ __forceinline__ float silu(float y) {
+  return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.44269504088896341f));
+}
 
 // The sequence that token t belongs to: the number of offsets[1..n] <= t.
 // The wave searches together, 64 probes a round.
@@ -131,14 +134,27 @@ __global__ __launch_bounds__(256) void k_conv(const ConvArgs a, int ctiles, int 
           const int seen = t - start;         // tokens of the sequence before this one
           if (seq < a.n && seen >= (a.window ? W - 1 : 0) && !skip) {
             VT y;
+            float s[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              float s = bias[e];
+            for (int e = 0; e < V; ++e) s[e] = bias[e];
+            if (seen >= W - 1) {
 #pragma unroll
               for (int j = 0; j < W; ++j)
-                if (seen >= W - 1 - j) s = fmaf(w[j][e], Elem<BF16>::get(r[i + j].e[e]), s);
-              y.e[e] = Elem<BF16>::put(a.silu ? silu(s) : s);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[e] = fmaf(w[j][e], Elem<BF16>::get(r[i + j].e[e]), s[e]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < W; ++j)
+                if (seen >= W - 1 - j)
+#pragma unroll
+                  for (int e = 0; e < V; ++e) s[e] = fmaf(w[j][e], Elem<BF16>::get(r[i + j].e[e]), s[e]);
             }
+            if (a.silu) {
+#pragma unroll
+              for (int e = 0; e < V; ++e) s[e] = silu(s[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) y.e[e] = Elem<BF16>::put(s[e]);
             VT* to = (VT*)(out + (int64_t)t * a.out_stride + c);
             // nontemporal: a long prompt's outputs are more than the caches hold
             // (16384 x 12288 bf16: 3% faster; 4011 x 2304 fp32: 6%)
