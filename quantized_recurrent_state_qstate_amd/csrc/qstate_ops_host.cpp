@@ -323,7 +323,7 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   a.os = c->out_stride;
   const int64_t v = 16 / es;
   const int64_t far = int64_t(1) << 24;   // the kernels keep offsets within 64 rows in 32 bits
-  if (p.chunked && T > 1 && (c->q_stride > far || c->k_stride > far || c->v_stride > far))
+  if (p.chunked && T > 1 && (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->out_stride > far))
     return op_fail(QS_EUNSUPPORTED, "a stride of more than 2^24 elements");
   a.vec = aligned(c->q, 16) && aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->out, 16) && vw % v == 0 &&
           a.dv % v == 0 && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0 && c->v_stride % v == 0 &&

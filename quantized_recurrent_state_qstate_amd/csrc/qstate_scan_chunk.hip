@@ -40,7 +40,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
   __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? kL * kKR : 8];
   __shared__ __attribute__((aligned(16))) uint16_t sv[kL * kVR];           // v, then the outputs
   __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 2 : 1][OUT ? kL * kPR : 8];   // P's two pieces
-  __shared__ double sc[kL];
+  __shared__ __attribute__((aligned(16))) float sc[2][kL];                 // c_i as a sum of two floats
   __shared__ __attribute__((aligned(16))) float se[kL], sw[kL], sb[kL];    // 2^{c_i}, weight in the update, beta
   __shared__ int sodd;
 
@@ -69,6 +69,9 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
       if (from && v < a.dv) S[n][t] = *(const F4*)(from + (head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
     }
   }
+  // the pieces this thread brings: rows kr, kr + kKStep, ..., column kc on; the same for v
+  constexpr int kKStep = kT * 8 / DK, kVStep = kT * 8 / kDV;
+  const int kr = tid / (DK / 8), kc = tid % (DK / 8) * 8, vr = tid / (kDV / 8), vc = tid % (kDV / 8) * 8;
   U4 nk[kKP], nq[OUT ? kKP : 1], nv[kVP];
   float nd = 1.0f, nb = 0.0f;
   auto fetch = [&](int t, int t1) {
@@ -78,15 +81,11 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
-      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-      nk[i] = tk.load(r, c);
-      if constexpr (OUT) nq[i] = tq.load(r, c);
+      nk[i] = tk.load_step(kr, kc, i, kKStep);
+      if constexpr (OUT) nq[i] = tq.load_step(kr, kc, i, kKStep);
     }
 #pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      nv[i] = tv.load(r, c);
-    }
+    for (int i = 0; i < kVP; ++i) nv[i] = tv.load_step(vr, vc, i, kVStep);
     nd = 1.0f;
     nb = 0.0f;
     if (tid < kL && t + tid < t1) {
@@ -140,19 +139,16 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     const bool whole = !OUT || sodd == 0;
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
-      const int p = i * kT + tid, r = p / (DK / 8), c = p % (DK / 8) * 8;
-      *(U4*)&sk[r * kKR + c] = nk[i];
-      if constexpr (OUT) *(U4*)&sq[r * kKR + c] = nq[i];
+      *(U4*)&sk[kr * kKR + kc + i * (kKStep * kKR)] = nk[i];
+      if constexpr (OUT) *(U4*)&sq[kr * kKR + kc + i * (kKStep * kKR)] = nq[i];
     }
 #pragma unroll
-    for (int i = 0; i < kVP; ++i) {
-      const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-      *(U4*)&sv[r * kVR + c] = nv[i];
-    }
+    for (int i = 0; i < kVP; ++i) *(U4*)&sv[vr * kVR + vc + i * (kVStep * kVR)] = nv[i];
     if (wave == 0) {
       const double c = wave_sums(nd == 0.0f ? -10000.0 : (double)log2f(nd));
       const double all = __shfl(c, 63);
-      sc[lane] = c;
+      sc[0][lane] = (float)c;
+      sc[1][lane] = (float)(c - (double)(float)c);
       sb[lane] = nb;
       se[lane] = __builtin_amdgcn_exp2f((float)c);
       sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * nb;
@@ -161,9 +157,8 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     if (OUT && tid == 0) sodd = 0;           // read by all, and next written behind the chunk's last barrier
     const int next = t + n;
     if (next < sg.t1) fetch(next, sg.t1);
-    const double call = sc[kL - 1];
-    total += call;
-    const float eall = __builtin_amdgcn_exp2f((float)call);
+    if constexpr (!OUT) total += (double)sc[0][kL - 1] + (double)sc[1][kL - 1];
+    const float eall = se[kL - 1];
 
     if (OUT && !whole) {
 #pragma unroll
@@ -183,7 +178,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
       for (int x = 0; x < 4 / WAVES; ++x) {
         const int it = WAVES == 4 ? wave : (x ? 3 - wave : wave);
         const int i = 16 * it + m;
-        const double ci = sc[i];
+        const float ci = sc[0][i], di = sc[1][i];
         // two tiles at a time, to the end of the step of 32 that the products below
         // read: right of the diagonal they become zeros
         for (int jp = 0; jp <= it; jp += 2) {
@@ -201,14 +196,12 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           for (int y = 0; y < 2; ++y) {
             const int j = 16 * (jp + y) + 4 * q4;
             const F4 bj = *(const F4*)&sb[j];
-            double cj[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) cj[r] = sc[j + r];
+            const F4 cj = *(const F4*)&sc[0][j], dj = *(const F4*)&sc[1][j];
             uint32_t hi[2], lo[2];
             float f[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float e = __builtin_amdgcn_exp2f((float)(ci - cj[r]));
+              const float e = __builtin_amdgcn_exp2f((ci - cj[r]) + (di - dj[r]));
               const float w = p[y][r] * e * bj[r];
               f[r] = j + r <= i ? w : 0.0f;
             }
@@ -259,13 +252,13 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           for (int r = 0; r < 4; ++r) O[v][i][r] *= e[r];
       }
       // ---- outputs: P u on top
+      BF8 ub[2][NV];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        BF8 ub[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
-          ub[v] = join(read_tr(x), read_tr(x + 16 * kVR));
+          ub[c][v] = join(read_tr(x), read_tr(x + 16 * kVR));
         }
         BF8 ph[4], pl[4];
 #pragma unroll
@@ -281,31 +274,33 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
           for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int i = 2 * c; i < 4; ++i)
-              O[v][i] = mfma(x ? pl[i] : ph[i], ub[v], O[v][i]);
+              O[v][i] = mfma(x ? pl[i] : ph[i], ub[c][v], O[v][i]);
       }
-      // ---- the state update (below) still reads v; only then the outputs take its place
-      F4 W[2][2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) W[c][j] = *(const F4*)&sw[32 * c + 16 * j + 4 * q4];
+      // ---- weighted v; then the outputs take v's place
       BF8 wu[NV][2][3];
-      const float skip = a.skip ? a.skip[h] : 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
+        F4 W[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) W[j] = *(const F4*)&sw[32 * c + 16 * j + 4 * q4];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
-          const BF8 y = join(read_tr(x), read_tr(x + 16 * kVR));
           float f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float vv = (float)y[j];
-            f[j] = W[c][j >> 2][j & 3] * vv;
-            if (a.skip) O[v][2 * c + (j >> 2)][j & 3] = fmaf(skip, vv, O[v][2 * c + (j >> 2)][j & 3]);
-          }
+          for (int j = 0; j < 8; ++j) f[j] = W[j >> 2][j & 3] * (float)ub[c][v][j];
           split(f, wu[v][c]);
         }
+      }
+      if (a.skip) {
+        const float skip = a.skip[h];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              O[v][2 * c + (j >> 2)][j & 3] = fmaf(skip, (float)ub[c][v][j], O[v][2 * c + (j >> 2)][j & 3]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -333,21 +328,9 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     }
     if constexpr (OUT) {
       __syncthreads();                       // outputs are in LDS, the chunk has been read
+      const Tile<VEC> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
 #pragma unroll
-      for (int i = 0; i < kVP; ++i) {
-        const int p = i * kT + tid, r = p / (kDV / 8), c = p % (kDV / 8) * 8;
-        if (r < n) {
-          const U4 y = *(const U4*)&sv[r * kVR + c];
-          uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
-          if constexpr (VEC) {
-            if (v0 + c < a.dv) *(U4*)(o + c) = y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (v0 + c + j < a.dv) o[c + j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
-          }
-        }
-      }
+      for (int i = 0; i < kVP; ++i) to.store_step(vr, vc, i, kVStep, *(const U4*)&sv[vr * kVR + vc + i * (kVStep * kVR)]);
     }
     t = next;
   }

@@ -156,6 +156,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
     if (tid < kVP) *(U4*)&sv[tid / (kDV / 8) * kVR + tid % (kDV / 8) * 8] = nv;
     __syncthreads();                         // products are there; the block before has been read
     // ---- the operands
+    uint32_t far = 0, high = 0;
     float before[kC], behind[kC];
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
@@ -177,10 +178,12 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         const float D = before[j] * pre[i][j], kb = nk[i][j] * nb[i];
-        bad = bad || !(D >= 0x1p-96f && D <= 0x1p96f && fabsf(kb) < INFINITY);
+        // D in [2^-96, 2^96] and kb finite, on the bits: the largest of each over the tokens
+        far = max(far, __float_as_uint(D) - 0x0F800000u);
+        high = max(high, __float_as_uint(kb) & 0x7FFFFFFFu);
         if constexpr (OUT) {
           x[j] = nq[i][j] * D;
-          y[j] = kb / D;
+          y[j] = kb * __builtin_amdgcn_rcpf(D);   // for P alone, of 16 bits
         }
         z[j] = kb * (suf[i][j] * behind[j]);
       }
@@ -194,7 +197,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
       put_piece<kC>(&su[1][r * kR + ch], z, false);
       put_piece<kC>(&su[2][r * kR + ch], z, true);
     }
-    if (OUT && bad) sodd[turn] = 1;
+    if (OUT && (bad || far > 0x60000000u || high >= 0x7F800000u)) sodd[turn] = 1;
     if (tid == 0) sodd[turn ^ 1] = 0;        // read in the block before, next written in the next
     __syncthreads();
     if (t + kB < sg.t1) fetch(t + kB);
@@ -274,9 +277,11 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
         for (int v = 0; v < NV; ++v) {
           O[v] = mfma16(__builtin_bit_cast(BF4, hi), vf[v], O[v]);
           O[v] = mfma16(__builtin_bit_cast(BF4, lo), vf[v], O[v]);
+          if (a.skip)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[v][r] = fmaf(skip, (float)vf[v][r], O[v][r]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if (a.skip) O[v][r] = fmaf(skip, (float)vf[v][r], O[v][r]);
             const __bf16 y = (__bf16)O[v][r];
             so[(4 * q4 + r) * kVR + col + 16 * v] = __builtin_bit_cast(uint16_t, y);
           }
@@ -304,17 +309,8 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
     if constexpr (OUT) {
       if (tid < kVP) {
         const int r = tid / (kDV / 8), c = tid % (kDV / 8) * 8;
-        if (r < n) {
-          const U4 y = *(const U4*)&so[r * kVR + c];
-          uint16_t* o = (uint16_t*)a.out + (int64_t)(t + r) * a.os + head + v0;
-          if constexpr (VEC) {
-            if (v0 + c < a.dv) *(U4*)(o + c) = y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (v0 + c + j < a.dv) o[c + j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
-          }
-        }
+        const Tile<VEC> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
+        to.store_step(r, c, 0, 0, *(const U4*)&so[r * kVR + c]);
       }
     }
   }

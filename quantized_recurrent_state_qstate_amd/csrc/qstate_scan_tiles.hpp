@@ -157,6 +157,28 @@ struct Tile {
       return (U4){d[0], d[1], d[2], d[3]};
     }
   }
+  // Piece i of several that lie `step` rows apart from row r on: one product, then sums.
+  __device__ __forceinline__ U4 load_step(int r, int c, int i, int step) const {
+    if constexpr (VEC) {
+      const int at = (r * stride + c) * 2 + i * (step * stride * 2);
+      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+    } else {
+      return load(r + i * step, c);
+    }
+  }
+  // The same way back; nothing at or behind the bound, or from column `width` on.
+  __device__ __forceinline__ void store_step(int r, int c, int i, int step, U4 y) const {
+    if constexpr (VEC) {
+      const uint32_t at = c < width ? (uint32_t)((r * stride + c) * 2) : 0x80000000u;
+      __builtin_amdgcn_raw_buffer_store_b128(y, rsrc, at + (uint32_t)(i * (step * stride * 2)), 0, 0);
+    } else {
+      uint16_t* o = (uint16_t*)p + (int64_t)(r + i * step) * stride + c;
+      if (r + i * step < n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < width) o[j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+    }
+  }
   // Elements e .. e + 511 of an LDS tile with rows of N, as at<N>() lays them, by one wave.
   template <int N>
   __device__ __forceinline__ void bring(uint16_t* tile, int e, int lane) const {
