@@ -6,9 +6,13 @@
 //   its window (the last W-1 rows of what it has seen), which the call
 //   replaces by the new last W-1 rows.
 //
-// Sums in fp32, one rounding to the output type.  Both kernels are bound by
-// HBM: every x row is read once from HBM (the W-1 rows that neighbouring runs
-// share come from the cache), every y row written once.
+// Sums in fp32, one rounding to the output type.  Bound by HBM: every x row is
+// read once (the W-1 rows that neighbouring runs share come from the cache),
+// every y row written once.  A thread keeps 8 (fp32: 4) channels and their
+// weights over a run of tokens, so a wave reads and writes 1 KB a row.  16384
+// tokens of 12288 channels in bf16: 172 us, 4.7 TB/s where a copy of 1 GiB
+// reaches 5.2; 4011 of 2304 in fp32: 15 us, 4.9 TB/s.  One token for 8 sequences
+// of 2304 channels: 3.9 us, a launch and one trip to memory.
 #include <hip/hip_runtime.h>
 
 #include "qstate_ops.hpp"

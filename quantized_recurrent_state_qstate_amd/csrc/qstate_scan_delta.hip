@@ -18,7 +18,13 @@
 // of u in the update, two (16 bits) of S, P and u in the outputs, which are
 // rounded to bf16 at the end.  T is fp32, made and applied by fp32 matrix
 // instructions: its diagonal blocks of 16 by substitution, the others from
-// them.  c is summed in fp64; a decay of zero counts as 2^-10000.
+// them; it is applied as three bf16 pieces by three of R, the six products that
+// reach 24 bits.  c is summed in fp64; a decay of zero counts as 2^-10000.
+//
+// One sequence of 7868 tokens, 32 heads of 128 x 128: 54 us for the first launch,
+// 440 for the second, 3.6 us a chunk, of which 182 matrix instructions of a
+// wave (16 cycles each) are a third and their operands' splitting into pieces a
+// quarter, one after the other in the one wave a SIMD has.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
