@@ -65,8 +65,10 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
   F4 S[NV][2 * kKS];
   const int vcol = (wave * NV) * 16 + m;
   const float* from = !OUT ? nullptr
-                      : sg.first ? (a.initial ? a.initial + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
-                                 : g.states + (int64_t)s * a.H * a.dv * DK;
+                      // a sequence in one piece; of several, the first one's state is kept with the
+                      // others, since the last one may write it over (final may be initial)
+                      : sg.first && sg.last ? (a.initial ? a.initial + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
+                                            : g.states + (int64_t)s * a.H * a.dv * DK;
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int v = v0 + vcol + 16 * n;
@@ -392,7 +394,7 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (c + i >= c1) break;
-      if (c + i > c0) st[(int64_t)(c + i + seq) * all + e] = S;   // what was there is in L
+      st[(int64_t)(c + i + seq) * all + e] = S;   // what was there is in L
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[r] = fmaf(d[i][r], S[r], L[i][r]);
     }

@@ -96,8 +96,10 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
   F4 S[NV][2 * kKS];
   const int col = (wave * NV) * 16 + m;
   const float* from = !OUT ? nullptr
-                      : sg.first ? (a.initial ? a.initial + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
-                                 : g.states + (int64_t)s * a.H * a.dv * DK;
+                      // a sequence in one piece; of several, the first one's state is kept with the
+                      // others, since the last one may write it over (final may be initial)
+                      : sg.first && sg.last ? (a.initial ? a.initial + (int64_t)sg.seq * a.H * a.dv * DK : nullptr)
+                                            : g.states + (int64_t)s * a.H * a.dv * DK;
 #pragma unroll
   for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -350,8 +352,11 @@ hipError_t key(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 
 template <int DK>
 hipError_t key_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  if (a.dv <= 64 || DK == 256) return a.vec ? key<DK, 1, true>(a, g, s) : key<DK, 1, false>(a, g, s);
-  return a.vec ? key<DK, 2, true>(a, g, s) : key<DK, 2, false>(a, g, s);
+  // 128 columns a workgroup halve the operands' preparation; 256 channels leave
+  // no registers for them
+  if constexpr (DK < 256)
+    if (a.dv > 64) return a.vec ? key<DK, 2, true>(a, g, s) : key<DK, 2, false>(a, g, s);
+  return a.vec ? key<DK, 1, true>(a, g, s) : key<DK, 1, false>(a, g, s);
 }
 
 }  // namespace

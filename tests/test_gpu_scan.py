@@ -289,3 +289,20 @@ def test_scan_long_and_many_heads(kind):
     """Long enough to be cut into segments, over cells' and sequences' boundaries."""
     run(kind, "head", [700, 1, 0, 1300, 64, 47], 4, 2, 64, 40, "bf16", initial=True, skip=True, mu=5.0)
     run(kind, "head", [2048], 2, 1, 128, 64, "bf16", mu=6.0)
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+def test_scan_in_place_over_many_segments(kind, decay):
+    """final may be initial: the state before a sequence's first segment is read from it while the last segment, a
+    single token here, is done long before."""
+    dk, dv, H, T = 64, 64, 32, 4097
+    q, k, v, d, b = (x.to(DEV) for x in inputs(kind, decay, [T], H, 1, dk, dv, "bf16", mu=6.0))
+    qs = QState(StateConfig(kind=kind, decay_mode=decay, B=1, H=H, dk=dk, dv=dv))
+    S0 = torch.randn(1, H, dv, dk, device=DEV) * 100
+    out, fin = qs.scan(q, k, v, d, b, initial=S0)
+    for _ in range(5):
+        S = S0.clone()
+        o, f = qs.scan(q, k, v, d, b, initial=S, final=S)
+        torch.cuda.synchronize()
+        assert torch.equal(o, out) and torch.equal(f, fin)
+    qs.close()
