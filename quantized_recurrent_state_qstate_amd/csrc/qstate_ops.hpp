@@ -92,9 +92,8 @@ struct ScanArgs {
   int32_t bf16, delta, key;
   int32_t vec;             // q, k, v and out rows allow 16-byte accesses
 };
-hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
-// Segments of the chunked scans: cells of `seg` tokens of the packed axis,
+// Segments of the scans: cells of `seg` tokens of the packed axis,
 // cut again where sequences begin; `count` bounds their number.  Delta rule:
 // seg is a chunk's 64 tokens, states its prepared matrices.
 struct ScanSegs {
@@ -106,6 +105,7 @@ constexpr int kScanPrepBytes = 1024 + 18 * 1024 + 12 * 1024;
 hipError_t launch_scan_key(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
+hipError_t launch_scan(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 
 }  // namespace qs

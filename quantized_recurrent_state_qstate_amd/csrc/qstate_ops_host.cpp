@@ -220,7 +220,11 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
 // so it has at least 256 tokens (one decay a head; 16384 tokens of 32 heads of
 // 128 x 64: 140 us with segments for 512 workgroups, 155 us for 1024, 175 us
 // for 384) or 128 (a decay a channel, whose blocks are slower; 2048 tokens of
-// 32 heads of 128 x 128: 118 us for 1024, 164 us with at least 256 tokens).
+// 32 heads of 128 x 128: 118 us for 1024, 164 us with at least 256 tokens) or,
+// token by token, 64 (fp32, 2048 tokens of 8 heads of 64 x 64: 53 us, 62 with
+// at least 128, 464 uncut), there only if the sequences have two segments on
+// the average (16 of 64 tokens: 25 us cut, 19 not; of 32 heads of 128 x 128:
+// 81, 68).
 struct ScanPlan {
   bool chunked;
   qs::ScanSegs segs;
@@ -233,16 +237,18 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= (int64_t)a.n * (a.delta ? 48 : 16);
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
-  if (!p.chunked) return p;
+  if (a.delta && !p.chunked) return p;
   if (a.delta) {
     p.segs.seg = 64;
     p.segs.count = (a.T + 63) / 64 + a.n;
     p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)qs::kScanPrepBytes;
     return p;
   }
-  const int64_t work = (int64_t)a.T * a.H * ((a.dv + 63) / 64);
-  const int64_t seg = std::max<int64_t>(a.key ? 128 : 256, (work / (a.key ? 1024 : 512) + 63) / 64 * 64);
-  if (seg >= a.T) return p;
+  const int columns = p.chunked ? 64 : 32;     // a workgroup's
+  const int64_t work = (int64_t)a.T * a.H * ((a.dv + columns - 1) / columns);
+  const int64_t least = !p.chunked ? 64 : a.key ? 128 : 256, groups = p.chunked && !a.key ? 512 : 1024;
+  const int64_t seg = std::max<int64_t>(least, (work / groups + 63) / 64 * 64);
+  if (seg >= a.T || (!p.chunked && 2 * seg * a.n > a.T)) return p;
   p.segs.seg = (int32_t)seg;
   p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);
   p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)a.dv * (uint64_t)a.dk * 4u;
@@ -331,7 +337,7 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
   hipError_t e = p.chunked ? (a.delta ? qs::launch_scan_delta : a.key ? qs::launch_scan_key : qs::launch_scan_chunk)(
                                  a, p.segs, reinterpret_cast<hipStream_t>(stream))
-                           : qs::launch_scan(a, reinterpret_cast<hipStream_t>(stream));
+                           : qs::launch_scan(a, p.segs, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));
   return op_ok();
 }

@@ -10,12 +10,15 @@
 // registers.  Sums over channels are 16-lane DPP reductions.  Everything is
 // fp32.
 //
-// Bound by the chain from token to token (two reductions by the delta rule):
-// about 0.3 us a token, 9.6 us for 32 tokens of 2 heads of 64 x 64.  It carries
-// fp32 prompts, short ones, and the delta rule with a decay a channel.
+// It carries fp32 prompts, short ones, and the delta rule with a decay a
+// channel.  Bound by the chain from token to token (a reduction in it by the
+// delta rule, which cannot be cut): about 0.19 us a token, 378 us for 2048
+// tokens of 8 heads of 64 x 64.  Additive sequences are cut into segments: one
+// pass for the states that the segments add (no queries, no outputs), the join,
+// one pass for the outputs; 53 us against 464 us uncut for the same sizes.
 #include <hip/hip_runtime.h>
 
-#include "qstate_ops.hpp"
+#include "qstate_scan_tiles.hpp"
 
 namespace qs {
 namespace {
@@ -64,25 +67,33 @@ __device__ __forceinline__ void get(const void* p, int64_t i, bool vec, float (&
   }
 }
 
-template <int BF16, int DK, bool DELTA, bool KEY, int RPL>
-__global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
+template <int BF16, int DK, bool DELTA, bool KEY, int RPL, bool OUT>
+__global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs gs, int rchunks) {
   constexpr int kRows = 16 * RPL;
   constexpr int kEl = kStage * DK / 256;   // staged elements a thread brings, of each of q, k, decay
   constexpr int kTh = DK / kEl;            // threads a token's row takes (16)
   constexpr int kM = DK / 64;              // groups of 4 channels a lane holds
   constexpr int kV = kStage * kRows / 256; // staged elements of v a thread brings
   static_assert(kTh == 16, "16 threads bring one token");
-  __shared__ float sk[kStage][DK], sq[kStage][DK], sd[KEY ? kStage : 1][KEY ? DK : 1];
-  __shared__ float sv[kStage][kRows], so[kStage][kRows], sg[kStage], sb[kStage];
+  __shared__ float sk[kStage][DK], sq[OUT ? kStage : 1][OUT ? DK : 1], sd[KEY ? kStage : 1][KEY ? DK : 1];
+  __shared__ float sv[kStage][kRows], so[OUT ? kStage : 1][OUT ? kRows : 1], sg[kStage], sb[kStage];
   const int tid = (int)threadIdx.x;
-  const int rc = (int)blockIdx.x % rchunks, sh = (int)blockIdx.x / rchunks;
-  const int h = sh % a.H, seq = sh / a.H;
+  const int per = a.H * rchunks;
+  const int sid = (int)(blockIdx.x / (uint32_t)per), hr = (int)(blockIdx.x % (uint32_t)per);
+  const int h = hr / rchunks, rc = hr % rchunks;
   const int g = h / (a.H / a.G);
-  const int t0 = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
-  const int t1 = a.offsets ? min(max(a.offsets[seq + 1], t0), a.T) : a.T;
+  const Segment seg = find_segment(a, gs.seg, sid);
+  if (seg.none || (!OUT && seg.last)) return;
+  const int t0 = seg.t0, t1 = seg.t1;
   const int sub = tid & 15, row = (tid >> 4) * RPL;   // this lane's channels and first row
   const int r0 = rc * kRows;
-  const int64_t st = ((int64_t)seq * a.H + h) * a.dv;
+  const int64_t st = (int64_t)h * a.dv, states = (int64_t)a.H * a.dv * DK;
+  // a sequence in one piece begins with its own state; of several pieces all
+  // states are kept in the workspace (final may be initial)
+  const float* from = !OUT ? nullptr
+                      : seg.first && seg.last ? (a.initial ? a.initial + seg.seq * states : nullptr)
+                                              : gs.states + sid * states;
+  float* to = !OUT ? gs.states + sid * states : seg.last ? a.final + seg.seq * states : nullptr;
 
   float s[RPL][kM][4];
 #pragma unroll
@@ -90,22 +101,25 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
       float4 x = make_float4(0, 0, 0, 0);
-      if (a.initial && r0 + row + r < a.dv)
-        x = *(const float4*)(a.initial + (st + r0 + row + r) * DK + m * 64 + sub * 4);
+      if (from && r0 + row + r < a.dv)
+        x = *(const float4*)(from + (st + r0 + row + r) * DK + m * 64 + sub * 4);
       s[r][m][0] = x.x; s[r][m][1] = x.y; s[r][m][2] = x.z; s[r][m][3] = x.w;
     }
 
   // what this thread brings of a stage: token bt, channels bc..; v: rows of token vt
   const int bt = tid >> 4, bc = (tid & 15) * kEl;
-  float nk[kEl], nq[kEl], nd[KEY ? kEl : 1], nv[kV], ng = 1.0f, nb = 1.0f;
+  float nk[kEl], nq[OUT ? kEl : 1], nd[KEY ? kEl : 1], nv[kV], ng = 1.0f, nb = 1.0f;
   auto fetch = [&](int t) {
     const bool in = t + bt < t1;
     const int64_t tt = t + bt;
 #pragma unroll
-    for (int j = 0; j < kEl; ++j) nk[j] = nq[j] = 0.0f;
+    for (int j = 0; j < kEl; ++j) {
+      nk[j] = 0.0f;
+      if constexpr (OUT) nq[j] = 0.0f;
+    }
     if (in) {
       get<BF16>(a.k, tt * a.ks + (int64_t)g * DK + bc, a.vec, nk);
-      get<BF16>(a.q, tt * a.qs + (int64_t)g * DK + bc, a.vec, nq);
+      if constexpr (OUT) get<BF16>(a.q, tt * a.qs + (int64_t)g * DK + bc, a.vec, nq);
     }
     if constexpr (KEY) {
 #pragma unroll
@@ -117,12 +131,18 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
       nv[j] = (t + vt < t1 && r0 + vr < a.dv) ? get1<BF16>(a.v, (int64_t)(t + vt) * a.vs + (int64_t)h * a.dv + r0 + vr)
                                               : 0.0f;
     }
+    ng = nb = 1.0f;
     if (tid < kStage && t + tid < t1) {
       if constexpr (!KEY) ng = a.decay[(int64_t)(t + tid) * a.ds + h];
       nb = a.beta ? a.beta[(int64_t)(t + tid) * a.bs + h] : 1.0f;
     }
   };
 
+  float all[KEY ? kM : 1][4];
+#pragma unroll
+  for (int m = 0; m < (KEY ? kM : 1); ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) all[m][e] = 1.0f;
   fetch(t0);
   const float skip = a.skip ? a.skip[h] : 0.0f;
   for (int t = t0; t < t1; t += kStage) {
@@ -130,7 +150,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
 #pragma unroll
     for (int j = 0; j < kEl; j += 4) {
       *(float4*)&sk[bt][bc + j] = make_float4(nk[j], nk[j + 1], nk[j + 2], nk[j + 3]);
-      *(float4*)&sq[bt][bc + j] = make_float4(nq[j], nq[j + 1], nq[j + 2], nq[j + 3]);
+      if constexpr (OUT) *(float4*)&sq[bt][bc + j] = make_float4(nq[j], nq[j + 1], nq[j + 2], nq[j + 3]);
       if constexpr (KEY) *(float4*)&sd[bt][bc + j] = make_float4(nd[j], nd[j + 1], nd[j + 2], nd[j + 3]);
     }
 #pragma unroll
@@ -142,13 +162,16 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
     __syncthreads();
     fetch(t + kStage);                     // reads nothing at or behind t1
     const int n = min(kStage, t1 - t);
-    for (int i = 0; i < n; ++i) {
-      float kk[kM][4], qq[kM][4], dd[kM][4];
+    auto token = [&](int i) {
+      float kk[kM][4], qq[OUT ? kM : 1][4], dd[KEY ? kM : 1][4];
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        const float4 x = *(const float4*)&sk[i][m * 64 + sub * 4], y = *(const float4*)&sq[i][m * 64 + sub * 4];
+        const float4 x = *(const float4*)&sk[i][m * 64 + sub * 4];
         kk[m][0] = x.x; kk[m][1] = x.y; kk[m][2] = x.z; kk[m][3] = x.w;
-        qq[m][0] = y.x; qq[m][1] = y.y; qq[m][2] = y.z; qq[m][3] = y.w;
+        if constexpr (OUT) {
+          const float4 y = *(const float4*)&sq[i][m * 64 + sub * 4];
+          qq[m][0] = y.x; qq[m][1] = y.y; qq[m][2] = y.z; qq[m][3] = y.w;
+        }
         if constexpr (KEY) {
           const float4 z = *(const float4*)&sd[i][m * 64 + sub * 4];
           dd[m][0] = z.x; dd[m][1] = z.y; dd[m][2] = z.z; dd[m][3] = z.w;
@@ -163,7 +186,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
         for (int m = 0; m < kM; ++m)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[r][m][e] *= KEY ? dd[m][e] : d;
+            s[r][m][e] *= KEY ? dd[KEY ? m : 0][e] : d;
             if constexpr (DELTA) w = fmaf(s[r][m][e], kk[m][e], w);
           }
         float u = sv[i][row + r];
@@ -175,20 +198,39 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[r][m][e] = fmaf(u, kk[m][e], s[r][m][e]);
-            o[r] = fmaf(s[r][m][e], qq[m][e], o[r]);
+            if constexpr (OUT) o[r] = fmaf(s[r][m][e], qq[OUT ? m : 0][e], o[r]);
           }
-        o[r] = sum16(o[r]);
+        if constexpr (OUT) o[r] = sum16(o[r]);
       }
+      if constexpr (OUT)
 #pragma unroll
-      for (int r = 0; r < RPL; ++r)
-        if (sub == r) so[i][row + r] = o[r];
+        for (int r = 0; r < RPL; ++r)
+          if (sub == r) so[i][row + r] = o[r];
+      if constexpr (!OUT) {                  // the segment's whole decay
+        if constexpr (KEY) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) all[m][e] *= dd[m][e];
+        } else {
+          all[0][0] *= d;
+        }
+      }
+    };
+    // four tokens at a time, so that the next ones' channels are read meanwhile
+    int i = 0;
+    for (; i + 4 <= n; i += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) token(i + j);
     }
+    for (; i < n; ++i) token(i);
+    if constexpr (!OUT) continue;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       const int e = j * 256 + tid, vt = e / kRows, vr = e % kRows;
       if (vt < n && r0 + vr < a.dv) {
-        const float y = fmaf(skip, sv[vt][vr], so[vt][vr]);
+        const float y = fmaf(skip, sv[vt][vr], so[OUT ? vt : 0][OUT ? vr : 0]);
         const int64_t at = (int64_t)(t + vt) * a.os + (int64_t)h * a.dv + r0 + vr;
         if constexpr (BF16) {
           const __bf16 b = (__bf16)y;
@@ -199,36 +241,68 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, int rchunks) {
       }
     }
   }
+  if (to)
 #pragma unroll
-  for (int r = 0; r < RPL; ++r)
-    if (r0 + row + r < a.dv)
+    for (int r = 0; r < RPL; ++r)
+      if (r0 + row + r < a.dv)
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+          *(float4*)(to + (st + r0 + row + r) * DK + m * 64 + sub * 4) =
+              make_float4(s[r][m][0], s[r][m][1], s[r][m][2], s[r][m][3]);
+  if (!OUT && rc == 0 && tid < 16) {
+    if constexpr (KEY) {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
-        *(float4*)(a.final + (st + r0 + row + r) * DK + m * 64 + sub * 4) =
-            make_float4(s[r][m][0], s[r][m][1], s[r][m][2], s[r][m][3]);
+        *(float4*)&gs.total[((int64_t)sid * a.H + h) * DK + m * 64 + sub * 4] =
+            make_float4(all[m][0], all[m][1], all[m][2], all[m][3]);
+    } else if (tid == 0) {
+      gs.total[(int64_t)sid * a.H + h] = all[0][0];
+    }
+  }
 }
 
-template <int BF16, int DK, bool DELTA, bool KEY>
-hipError_t scan(const ScanArgs& a, hipStream_t s) {
-  constexpr int RPL = 2;
+template <int BF16, int DK, bool DELTA, bool KEY, int RPL>
+hipError_t scan_rows(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int rchunks = (a.dv + 16 * RPL - 1) / (16 * RPL);
-  k_scan<BF16, DK, DELTA, KEY, RPL><<<dim3((uint32_t)(a.n * a.H * rchunks)), 256, 0, s>>>(a, rchunks);
+  const uint32_t grid = (uint32_t)(g.count * a.H * rchunks);
+  if constexpr (!DELTA) {
+    if (g.states) {
+      k_scan<BF16, DK, DELTA, KEY, RPL, false><<<dim3(grid), 256, 0, s>>>(a, g, rchunks);
+      const hipError_t e = launch_scan_join(a, g, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  k_scan<BF16, DK, DELTA, KEY, RPL, true><<<dim3(grid), 256, 0, s>>>(a, g, rchunks);
   return hipGetLastError();
 }
 
+// One row a lane has the shorter chain, two read the channels half as often.
+// Up to 16384 rows in all (1024 workgroups of one row a lane) the chain counts:
+// delta rule, one decay a head, 2048 tokens of 8 heads of 64 x 64: 378 us with
+// one, 548 us with two; of 32 heads of 128 x 128: 381, 551; 8 times 256 tokens
+// of 32 heads of 128 x 128 (32768 rows): 194, 179.
+template <int BF16, int DK, bool DELTA, bool KEY>
+hipError_t scan(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return (int64_t)g.count * a.H * a.dv <= 16384 ? scan_rows<BF16, DK, DELTA, KEY, 1>(a, g, s)
+                                                : scan_rows<BF16, DK, DELTA, KEY, 2>(a, g, s);
+}
+
 template <int BF16, int DK>
-hipError_t scan_dk(const ScanArgs& a, hipStream_t s) {
-  if (a.delta) return a.key ? scan<BF16, DK, true, true>(a, s) : scan<BF16, DK, true, false>(a, s);
-  return a.key ? scan<BF16, DK, false, true>(a, s) : scan<BF16, DK, false, false>(a, s);
+hipError_t scan_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  if (a.delta) return a.key ? scan<BF16, DK, true, true>(a, g, s) : scan<BF16, DK, true, false>(a, g, s);
+  return a.key ? scan<BF16, DK, false, true>(a, g, s) : scan<BF16, DK, false, false>(a, g, s);
 }
 
 template <int BF16>
-hipError_t scan_in(const ScanArgs& a, hipStream_t s) {
-  return a.dk == 64 ? scan_dk<BF16, 64>(a, s) : a.dk == 128 ? scan_dk<BF16, 128>(a, s) : scan_dk<BF16, 256>(a, s);
+hipError_t scan_in(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.dk == 64 ? scan_dk<BF16, 64>(a, g, s)
+                    : a.dk == 128 ? scan_dk<BF16, 128>(a, g, s) : scan_dk<BF16, 256>(a, g, s);
 }
 
 }  // namespace
 
-hipError_t launch_scan(const ScanArgs& a, hipStream_t s) { return a.bf16 ? scan_in<1>(a, s) : scan_in<0>(a, s); }
+hipError_t launch_scan(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.bf16 ? scan_in<1>(a, g, s) : scan_in<0>(a, g, s);
+}
 
 }  // namespace qs

@@ -48,7 +48,8 @@ const char* step_kernel_name(int, int, int, int, int) { return "stand-in"; }
 hipError_t launch_conv(const ConvArgs&, hipStream_t) { ++g_launches; return hipSuccess; }
 hipError_t launch_conv_step(const ConvArgs&, hipStream_t) { ++g_launches; return hipSuccess; }
 hipError_t launch_qk(const QkArgs&, hipStream_t) { ++g_launches; return hipErrorInvalidValue; }
-hipError_t launch_scan(const ScanArgs&, hipStream_t) { ++g_launches; g_chunked = 0; return hipSuccess; }
+hipError_t launch_scan(const ScanArgs&, const ScanSegs& s, hipStream_t) { ++g_launches; g_chunked = 0; g_segs = s; return hipSuccess; }
+hipError_t launch_scan_join(const ScanArgs&, const ScanSegs&, hipStream_t) { return hipSuccess; }
 hipError_t launch_scan_chunk(const ScanArgs&, const ScanSegs& s, hipStream_t) { ++g_launches; g_chunked = 1; g_segs = s; return hipSuccess; }
 hipError_t launch_scan_key(const ScanArgs&, const ScanSegs& s, hipStream_t) { ++g_launches; g_chunked = 2; g_segs = s; return hipSuccess; }
 hipError_t launch_scan_delta(const ScanArgs&, const ScanSegs& s, hipStream_t) { ++g_launches; g_chunked = 3; g_segs = s; return hipSuccess; }
@@ -123,7 +124,8 @@ int main() {
         CHECK(qstate_scan_workspace(h, &a, &need) == QS_OK);
         CHECK(qstate_scan(h, &a, ws, need, nullptr) == QS_OK);
         const bool chunked = dtype == QS_BF16 && !(kind == QS_KIND_DELTA && decay == QS_DECAY_KEY);
-        CHECK((g_chunked != 0) == chunked && (need > 0) == chunked);
+        CHECK((g_chunked != 0) == chunked);
+        CHECK((need > 0) == (chunked || kind == QS_KIND_ADDITIVE) && (need > 0) == (g_segs.states != nullptr));
         if (need) {
           CHECK(qstate_scan(h, &a, nullptr, need, nullptr) == QS_EINVAL);
           CHECK(qstate_scan(h, &a, ws + 16, need, nullptr) == QS_EINVAL);
@@ -199,9 +201,8 @@ int main() {
           a.final = (float*)at(5000ull << 32);
           a.initial = nullptr;
           CHECK(qstate_scan_workspace(h, &a, &need) == QS_OK);
-          g_chunked = 0;
           CHECK(qstate_scan(h, &a, at(6000ull << 32), need, nullptr) == QS_OK);
-          if (g_chunked) {
+          {
             const int64_t seg = g_segs.seg;
             CHECK(seg > 0 && g_segs.count >= ((seg < T ? (T - 1) / seg : 0) + n));
             if (g_segs.states) {

@@ -306,3 +306,48 @@ def test_scan_in_place_over_many_segments(kind, decay):
         torch.cuda.synchronize()
         assert torch.equal(o, out) and torch.equal(f, fin)
     qs.close()
+
+
+@pytest.mark.parametrize("decay", ["head", "key"])
+@pytest.mark.parametrize("dk,dv,H", [(64, 64, 4), (128, 33, 2), (256, 5, 2), (64, 100, 32)])
+def test_scan_fp32_in_segments(decay, dk, dv, H):
+    """Additive fp32 prompts long enough to be cut, in place, with sequences that end inside a segment."""
+    run("additive", decay, [300, 0, 1, 700, 64, 129], H, 2, dk, dv, "fp32", initial=True, skip=True, strided=True,
+        mu=5.0)
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scan_many_rows_of_short_sequences(kind, decay, dtype):
+    """More rows than one a lane is taken for, lengths that are not whole groups of tokens."""
+    run(kind, decay, [9, 0, 1, 18, 3, 15, 11], 32, 8, 64, 100, dtype, initial=True, skip=True)
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+def test_scan_fp32_later_tokens_do_not_reach_earlier_ones(kind, decay):
+    lengths, bad = [150, 180], 71
+    q, k, v, d, b = (x.to(DEV) for x in inputs(kind, decay, lengths, 2, 2, 64, 48, "fp32"))
+    qs = QState(StateConfig(kind=kind, decay_mode=decay, B=2, H=2, dk=64, dv=48, in_dtype="fp32"))
+    clean, cfin = qs.scan(q, k, v, d, b, offsets=offsets(lengths))
+    v[bad, 0, 3] = float("inf")
+    out, fin = qs.scan(q, k, v, d, b, offsets=offsets(lengths))
+    torch.cuda.synchronize()
+    ok = torch.ones_like(out, dtype=torch.bool)
+    ok[bad:150, 0, 3] = False
+    assert torch.equal(out[ok], clean[ok]) and not torch.isfinite(out[~ok]).any()
+    assert torch.equal(fin[1], cfin[1]) and torch.equal(fin[0, 1], cfin[0, 1]) and not torch.isfinite(fin[0, 0, 3]).all()
+    qs.close()
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+def test_scan_fp32_infinite_last_value(kind, decay):
+    """What the last token leaves in the state is stored as it is, whatever the length."""
+    for T in (1, 5, 16, 18):
+        q, k, v, d, b = (x.to(DEV) for x in inputs(kind, decay, [T], 1, 1, 64, 8, "fp32"))
+        v[T - 1, 0, 2] = float("inf")
+        qs = QState(StateConfig(kind=kind, decay_mode=decay, B=1, H=1, dk=64, dv=8, in_dtype="fp32"))
+        _, fin = qs.scan(q, k, v, d, b)
+        torch.cuda.synchronize()
+        assert torch.equal(fin[0, 0, 2], torch.where(k[T - 1, 0] > 0, 1.0, -1.0) * float("inf"))
+        assert torch.isfinite(fin[0, 0, [0, 1, 3, 4, 5, 6, 7]]).all()
+        qs.close()
