@@ -94,12 +94,14 @@ struct ScanArgs {
 };
 
 // Segments of the scans: cells of `seg` tokens of the packed axis,
-// cut again where sequences begin; `count` bounds their number.  Delta rule:
-// seg is a chunk's 64 tokens, states its prepared matrices.
+// cut again where sequences begin; `count` bounds their number.  Delta rule in
+// chunks: seg is a chunk's 64 tokens, states its prepared matrices; sequences
+// of more than two cells of `cut` tokens (0: none) are cut, total has for each
+// piece L and M, [dv + dk][dk] a head.
 struct ScanSegs {
-  int32_t seg, count;
+  int32_t seg, count, cut;
   float* states;           // [count][H][dv][dk], null: no sequence is cut; delta rule: [count][H] kScanPrepBytes
-  float* total;            // [count][H] or [count][H][dk]: a segment's whole decay
+  float* total;            // [count][H] or [count][H][dk]: a segment's whole decay; delta rule: L and M
 };
 constexpr int kScanPrepBytes = 1024 + 18 * 1024 + 12 * 1024;
 hipError_t launch_scan_key(const ScanArgs& a, const ScanSegs& g, hipStream_t s);

@@ -242,6 +242,18 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     p.segs.seg = 64;
     p.segs.count = (a.T + 63) / 64 + a.n;
     p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)qs::kScanPrepBytes;
+    // Pieces: as many as have their L and M made by 256 workgroups at once (the
+    // first needs no M, the last neither), of 512 tokens or more (dk 256: 1024; 4
+    // heads of 256 x 256, 2048 tokens: 210 us with 512, 187 in one piece).  One
+    // sequence of 8192 tokens: 2 heads of 128 x 128 105 us, in one piece 449; 8
+    // heads 146, 461; 32 heads 336, 513.  A batch with none that is long pays
+    // for launches that do nothing (8 of 1024 tokens, 16 heads: 106 us, 98).
+    const int64_t wide = (a.dv + 63) / 64, blocks = (int64_t)a.H * (wide + a.dk / 64);   // of one piece's L and M
+    const int64_t cut = std::max<int64_t>(std::max(512, 4 * a.dk), (a.T / (256 / blocks + 1) + 63) / 64 * 64);
+    if (blocks <= 128 && a.n * a.H * wide <= 256 && a.T > 2 * cut) {
+      p.segs.cut = (int32_t)cut;
+      p.total = (uint64_t)((a.T + cut - 1) / cut + a.n) * (uint64_t)a.H * (uint64_t)(a.dv + a.dk) * (uint64_t)a.dk * 4u;
+    }
     return p;
   }
   const int columns = p.chunked ? 64 : 32;     // a workgroup's

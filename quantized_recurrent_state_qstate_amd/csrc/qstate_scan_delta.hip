@@ -21,10 +21,14 @@
 // them; it is applied as three bf16 pieces by three of R, the six products that
 // reach 24 bits.  c is summed in fp64; a decay of zero counts as 2^-10000.
 //
-// One sequence of 7868 tokens, 32 heads of 128 x 128: 54 us for the first launch,
-// 440 for the second, 3.6 us a chunk, of which 182 matrix instructions of a
+// Where few heads leave compute units idle, long sequences go in pieces at once:
+// a pass for what each piece does to the state before it, a short chain over
+// the pieces, a pass for the outputs.  One sequence of 8192 tokens, 32 heads of
+// 128 x 128, in 3 pieces: 57 us for the first launch, 125, 9 and 181 for the
+// others, 4.2 us a chunk at the outputs, of which 182 matrix instructions of a
 // wave (16 cycles each) are a third and their operands' splitting into pieces a
-// quarter, one after the other in the one wave a SIMD has.
+// quarter, one after the other in the one wave a SIMD has; in one piece 513 us
+// in all.  2 heads, in 16 pieces: 105 us, in one 449.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -200,13 +204,37 @@ struct Chunk {
   float prep[kPrepFloats];
 };
 
-// One sequence's chunks in order; a workgroup holds 16 WAVES value columns of a
+// A piece of a sequence: of one of more than two cells the part in cell c, of any
+// other all of it.  Whether a sequence is cut depends on its offsets, which
+// the host does not know: a short one gains nothing.
+struct Piece {
+  int seq, t0, t1, cell;
+  bool first, last, none;
+};
+__device__ __forceinline__ bool long_enough(int start, int end, int cut) { return cut > 0 && (end - start + 1) / 2 > cut; }
+__device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
+  Segment g{s, 0, 0, true, true, false};
+  if (cut > 0) g = find_segment(a, cut, s);
+  const int start = a.offsets ? min(max(a.offsets[g.seq], 0), a.T) : 0;
+  const int end = a.offsets ? min(max(a.offsets[g.seq + 1], start), a.T) : a.T;
+  if (long_enough(start, end, cut)) return {g.seq, g.t0, g.t1, s, g.first, g.last, g.none};
+  return {g.seq, start, end, s, true, true, g.none || !g.first};
+}
+
+// A sequence's chunks in order; a workgroup holds 16 WAVES value columns of a
 // head, each wave 16 in accumulators [dk][v] (rows dealt so that a lane holds 8
 // channels in a row, the second operand of S k and S q as it is).  While a
 // chunk is worked on, the next one is on its way into the other buffer, from
 // memory to LDS directly; a chunk costs one barrier.
-template <int DK, int WAVES, bool VEC>
-__global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int vchunks) {
+//
+// Where few heads leave compute units idle, long sequences are cut into pieces.
+// A piece maps the state before it to S M + L.  The !OUT pass makes L (state
+// rows, from zero or the first piece's initial state) and M (further dk rows:
+// values of zero, from the identity) into `carry`, k_delta_join goes from
+// piece to piece, and the OUT pass makes the outputs of all pieces at once.
+template <int DK, int WAVES, bool VEC, bool OUT>
+__global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int cut, float* carry,
+                                                              int vchunks) {
   constexpr int kDV = 16 * WAVES, kKS = DK / 32;
   using Buf = Chunk<DK, kDV>;
   constexpr bool kTwo = 2 * sizeof(Buf) + WAVES * kL * 32 <= 160 * 1024;   // room for two buffers
@@ -215,39 +243,53 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   __shared__ __attribute__((aligned(16))) uint16_t so[WAVES][kL * 16];     // a wave's outputs
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, q4 = lane >> 4;
-  const int per = a.H * vchunks;
-  const int seq = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
-  const int h = hv % a.H, v0 = hv / a.H * kDV, kh = h / (a.H / a.G);
-  const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
-  const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
+  const int per = a.H * (OUT ? vchunks : vchunks + DK / kDV);
+  const int hv = (int)(blockIdx.x % (uint32_t)per), h = hv % a.H, kh = h / (a.H / a.G);
+  const Piece piece_of = find_piece(a, cut, (int)(blockIdx.x / (uint32_t)per));
+  const bool matrix = !OUT && hv / a.H >= vchunks;   // columns of M
+  const int v0 = matrix ? 0 : hv / a.H * kDV, m0 = matrix ? (hv / a.H - vchunks) * kDV : 0;
+  if (piece_of.none || (!OUT && (piece_of.last || (matrix && piece_of.first)))) return;
+  const int seq = piece_of.seq, start = piece_of.t0, end = piece_of.t1;
   const int64_t head = (int64_t)h * a.dv, st = (int64_t)seq * a.H * a.dv;
   const int col = wave * 16 + m, v = v0 + col;
   const float skip = a.skip ? a.skip[h] : 0.0f;
+  // this lane's row of the states given and kept, channels 8 q4 .. of every 32
+  const int64_t at_state = (st + head + v) * DK + 8 * q4;
+  const int64_t at_carry =
+      (((int64_t)piece_of.cell * a.H + h) * (a.dv + DK) + (matrix ? a.dv + m0 + col : v)) * DK + 8 * q4;
+  const bool real = matrix || v < a.dv;
+  const float* from = OUT && !(piece_of.first && piece_of.last) ? carry + at_carry
+                      : piece_of.first && a.initial             ? a.initial + at_state
+                                                                : nullptr;
+  float* to = !OUT ? carry + at_carry : piece_of.last ? a.final + at_state : nullptr;
 
   F4 S[2 * kKS];
 #pragma unroll
   for (int t = 0; t < 2 * kKS; ++t) {
     S[t] = (F4){0, 0, 0, 0};
-    if (a.initial && v < a.dv)
-      S[t] = *(const F4*)(a.initial + (st + head + v) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1));
+    if (matrix)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[t][r] = 32 * (t >> 1) + 8 * q4 + 4 * (t & 1) + r == m0 + col ? 1.0f : 0.0f;
+    else if (from && real) S[t] = *(const F4*)(from + 32 * (t >> 1) + 4 * (t & 1));
   }
 
   // The next chunk's pieces of 1 KB, `kPieces` for each wave, brought one by one.
-  constexpr int kK = kL * DK / 512 / WAVES, kV = kL * kDV / 512 / WAVES, kP = (kPrepFloats / 256 + WAVES - 1) / WAVES;
-  constexpr int kPieces = 2 * kK + kV + kP;
+  constexpr int kK = kL * DK / 512 / WAVES, kV = kL * kDV / 512 / WAVES, kQ = OUT ? kK : 0;
+  constexpr int kUsed = OUT ? kPrepFloats : kGate + kTri, kP = (kUsed / 256 + WAVES - 1) / WAVES;
+  constexpr int kPieces = kK + kQ + kV + kP;
   auto bringing = [&](Buf& b, int t, int t1) {   // piece i of the chunk from t to t1 into b
     const int rows = t1 - t;
     return [&b, wave, lane, tk = Tile<VEC>(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK),
             tq = Tile<VEC>(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK),
-            tv = Tile<VEC>(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0)),
+            tv = Tile<VEC>(a.v, (int64_t)t * a.vs + head + v0, a.vs, matrix ? 0 : rows, min(kDV, a.dv - v0)),
             tp = Tile<true>(prep, 2 * ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats, 0, min(rows, 1), kPrepFloats * 2)](
                int i) {
       if (i < kK) tk.template bring<DK>(b.k, (i * WAVES + wave) * 512, lane);
-      else if (i < 2 * kK) tq.template bring<DK>(b.q, ((i - kK) * WAVES + wave) * 512, lane);
-      else if (i < 2 * kK + kV) tv.template bring<kDV>(b.v, ((i - 2 * kK) * WAVES + wave) * 512, lane);
+      else if (i < kK + kQ) tq.template bring<DK>(b.q, ((i - kK) * WAVES + wave) * 512, lane);
+      else if (i < kK + kQ + kV) tv.template bring<kDV>(b.v, ((i - kK - kQ) * WAVES + wave) * 512, lane);
       else if (i < kPieces) {
-        const int e = (i - 2 * kK - kV) * WAVES + wave;
-        if (e < kPrepFloats / 256) to_lds(tp.rsrc, (uint16_t*)b.prep + e * 512, e * 1024 + lane * 16);
+        const int e = (i - kK - kQ - kV) * WAVES + wave;
+        if (e < kUsed / 256) to_lds(tp.rsrc, (uint16_t*)b.prep + e * 512, e * 1024 + lane * 16);
       }
     };
   };
@@ -295,7 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
         for (int i = 0; i < kPieces; ++i) bring(i);
       by_token<DK, true>(
           a, t, n, h, [&](int i, int c) { return *(const BF8*)&b.k[at<DK>(i, c)]; },
-          [&](int i, int c) { return *(const BF8*)&b.q[at<DK>(i, c)]; },
+          [&](int i, int c) { return *(const BF8*)&(OUT ? b.q : b.k)[at<DK>(i, c)]; },
           [&](int i) { return __uint_as_float((uint32_t)b.v[at<kDV>(i, col)] << 16); },
           [&](int i, float o) {
             const __bf16 y = (__bf16)o;
@@ -313,7 +355,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kf[c & 1][i] = *(const BF8*)&b.k[at<DK>(16 * i + m, 32 * c + 8 * q4)];
-        qf[c & 1][i] = *(const BF8*)&b.q[at<DK>(16 * i + m, 32 * c + 8 * q4)];
+        if constexpr (OUT) qf[c & 1][i] = *(const BF8*)&b.q[at<DK>(16 * i + m, 32 * c + 8 * q4)];
       }
     };
     BF8 sp[2][3];
@@ -335,7 +377,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           R[i] = mfma(kf[c & 1][i], sp[c & 1][y], R[i]);
-          if (y < 2) O[i] = mfma(qf[c & 1][i], sp[c & 1][y], O[i]);
+          if (OUT && y < 2) O[i] = mfma(qf[c & 1][i], sp[c & 1][y], O[i]);
         }
       if (c + 1 < kKS) pieces(c + 1);
     }
@@ -387,7 +429,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     for (int c = 0; c < 2; ++c) {
       BF8 P[4][2];
 #pragma unroll
-      for (int i = 2 * c; i < 4; ++i)
+      for (int i = 2 * c; OUT && i < 4; ++i)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
           P[i][y] = *(const BF8*)&b.prep[kGate + kTri + (2 * piece(i, c) + y) * kTile + lane * 4];
@@ -408,7 +450,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 #pragma unroll
       for (int y = 0; y < 3; ++y)
 #pragma unroll
-        for (int i = 2 * c; i < 4; ++i) O[i] = mfma(P[i][y == 1], ub[y == 2], O[i]);
+        for (int i = 2 * c; OUT && i < 4; ++i) O[i] = mfma(P[i][y == 1], ub[y == 2], O[i]);
       split(g, wu[c]);
     }
     // ---- the state
@@ -427,7 +469,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       for (int p = 0; p < 3; ++p)
 #pragma unroll
         for (int y = 0; y < 4; ++y) S[t4 + y] = mfma(kt[z & 1][y], wu[c][p], S[t4 + y]);
-      if (z < 2)                             // the outputs, behind the products that made them
+      if (OUT && z < 2)                      // the outputs, behind the products that made them
 #pragma unroll
         for (int i = 2 * z; i < 2 * z + 2; ++i)
 #pragma unroll
@@ -445,7 +487,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     __syncthreads();                         // this chunk is in LDS, and the one before has been read
     // behind the last chunk this is an empty one: the other buffer gets zeros
     const auto bring = bringing(other, next, min(next + kL, end));
-    put_out();
+    if constexpr (OUT) put_out();
     work(b, bring, t, next - t);
     done_t = t;
     done_n = next - t;
@@ -469,11 +511,93 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       step(buf0, buf0);
     }
   }
-  put_out();
-  if (v < a.dv)
+  if constexpr (OUT) put_out();
+  if (to && real)
 #pragma unroll
-    for (int y = 0; y < 2 * kKS; ++y)
-      *(F4*)(a.final + (st + head + v) * DK + 32 * (y >> 1) + 8 * q4 + 4 * (y & 1)) = S[y];
+    for (int y = 0; y < 2 * kKS; ++y) *(F4*)(to + 32 * (y >> 1) + 4 * (y & 1)) = S[y];
+}
+
+// From piece to piece of a sequence that is cut: the place of a piece's L takes
+// the state before it.  A workgroup has kJoinRows value rows of a head; its
+// groups of dk threads share the sum over S M's inner channel.  A piece waits
+// for the one before it, so its M and L are asked for one piece ahead: 16
+// pieces of 2 heads of 128 x 128 take 35 us (87 without, by 16 rows).
+constexpr int kJoinRows = 8;
+template <int DK>
+__global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, float* carry, int rchunks) {
+  constexpr int kGroups = 512 / DK, kJ = DK / kGroups, kE = kJoinRows * DK / 512;
+  __shared__ __attribute__((aligned(16))) float ss[kJoinRows][DK], sums[kGroups][kJoinRows * DK];
+  const int tid = (int)threadIdx.x;
+  const int per = a.H * rchunks;
+  const int seq = (int)(blockIdx.x / (uint32_t)per), hr = (int)(blockIdx.x % (uint32_t)per);
+  const int h = hr / rchunks, r0 = hr % rchunks * kJoinRows;
+  const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
+  const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
+  if (!long_enough(start, end, cut)) return;
+  const int c0 = start / cut, c1 = (end - 1) / cut;
+  auto piece_at = [&](int c) { return carry + ((int64_t)(c + seq) * a.H + h) * (a.dv + DK) * DK; };
+  // this thread's elements of the rows, tid + 512 e, and its part of M: a channel, kJ rows
+  const int ch = tid % DK, j0 = tid / DK * kJ;
+  const int rows = min(kJoinRows, a.dv - r0) * DK;   // elements there are
+  float S[kE], L[kE], w[kJ];
+  auto ask = [&](int c) {
+    typedef const __attribute__((address_space(1))) float* G;
+    G p = (G)piece_at(c);
+    asm("" : "+s"(p));                      // one base, or each load keeps an address of its own from piece to piece
+    const G M = p + (int64_t)a.dv * DK;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) L[e] = tid + 512 * e < rows ? p[(int64_t)r0 * DK + tid + 512 * e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) w[j] = (M + j * DK)[(uint32_t)(j0 * DK + ch)];
+  };
+  auto keep = [&](int c, int e, float x) {
+    if (tid + 512 * e < rows) piece_at(c)[(int64_t)r0 * DK + tid + 512 * e] = x;
+  };
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    const bool in = tid + 512 * e < rows;
+    const int64_t at = (((int64_t)seq * a.H + h) * a.dv + r0) * DK + tid + 512 * e;
+    S[e] = in ? piece_at(c0)[(int64_t)r0 * DK + tid + 512 * e] : 0.0f;   // began with the initial state
+    keep(c0, e, a.initial && in ? a.initial[at] : 0.0f);
+  }
+  ask(c0 + 1);
+  for (int c = c0 + 1; c < c1; ++c) {
+    float next[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      next[e] = L[e];
+      keep(c, e, S[e]);
+      (&ss[0][0])[tid + 512 * e] = S[e];
+    }
+    __syncthreads();
+    float acc[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) acc[r] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kJ; j += 4) {
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) {
+        const F4 x = *(const F4*)&ss[r][j0 + j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r] = fmaf(x[e], w[j + e], acc[r]);
+      }
+      // or all rows are read first, into more registers than there are
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) asm volatile("" : "+v"(acc[r]) : : "memory");
+    }
+    ask(min(c + 1, c1 - 1));
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) sums[tid / DK][r * DK + ch] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) next[e] += sums[i][tid + 512 * e];
+      S[e] = next[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) keep(c1, e, S[e]);
 }
 
 template <int DK, bool VEC>
@@ -484,7 +608,15 @@ hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
   k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
-  k_delta_scan<DK, WAVES, VEC><<<dim3((uint32_t)(a.n * a.H * vchunks)), 64 * WAVES, 0, s>>>(a, g.states, vchunks);
+  const int pieces = g.cut > 0 ? (a.T + g.cut - 1) / g.cut + a.n : a.n;
+  if (g.cut > 0) {
+    const int rchunks = (a.dv + kJoinRows - 1) / kJoinRows;
+    k_delta_scan<DK, WAVES, VEC, false><<<dim3((uint32_t)(pieces * a.H * (vchunks + DK / (16 * WAVES)))), 64 * WAVES, 0, s>>>(
+        a, g.states, g.cut, g.total, vchunks);
+    k_delta_join<DK><<<dim3((uint32_t)(a.n * a.H * rchunks)), 512, 0, s>>>(a, g.cut, g.total, rchunks);
+  }
+  k_delta_scan<DK, WAVES, VEC, true><<<dim3((uint32_t)(pieces * a.H * vchunks)), 64 * WAVES, 0, s>>>(
+      a, g.states, g.cut, g.total, vchunks);
   return hipGetLastError();
 }
 

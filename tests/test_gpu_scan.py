@@ -351,3 +351,45 @@ def test_scan_fp32_infinite_last_value(kind, decay):
         assert torch.equal(fin[0, 0, 2], torch.where(k[T - 1, 0] > 0, 1.0, -1.0) * float("inf"))
         assert torch.isfinite(fin[0, 0, [0, 1, 3, 4, 5, 6, 7]]).all()
         qs.close()
+
+
+@pytest.mark.parametrize("lengths", [[1537], [1024, 1025], [3, 1100, 0, 2600], [1600, 1600, 1600], [63, 4097, 1, 1024]])
+@pytest.mark.parametrize("dk,dv,H", [(64, 64, 4), (128, 33, 2), (256, 24, 2)])
+def test_scan_delta_in_pieces(lengths, dk, dv, H):
+    """Long sequences of few heads by the delta rule, in place: cut into pieces of whole chunks, or not, by their length;
+    last pieces of one token, sequences that begin inside a cell."""
+    run("delta", "head", lengths, H, 2, dk, dv, "bf16", initial=True, skip=True, strided=True, mu=5.0)
+    run("delta", "head", lengths, H, 1, dk, dv, "bf16", mu=2.0)
+
+
+@pytest.mark.parametrize("where,value", [("v", float("nan")), ("v", float("inf")), ("k", float("nan")),
+                                         ("decay", float("nan")), ("decay", 0.0), ("beta", float("inf"))])
+def test_scan_delta_in_pieces_odd_values(where, value):
+    """As in a sequence in one piece: a value that is not finite reaches its head (v: its row) from its token on, and a
+    decay of zero cuts off what was before."""
+    T, bad, H, dv = 2600, 1300, 2, 48
+    names = ("q", "k", "v", "decay", "beta")
+    args = dict(zip(names, (x.to(DEV) for x in inputs("delta", "head", [T], H, 2, 64, dv, "bf16", mu=6.0))))
+    qs = QState(StateConfig(kind="delta", decay_mode="head", B=1, H=H, dk=64, dv=dv))
+    S0 = torch.randn(1, H, dv, 64, device=DEV)
+    scan = lambda a, S, t0=0: qs.scan(*(a[n][t0:] for n in names), initial=S)
+    clean, cfin = scan(args, S0)
+    args[where] = args[where].clone()
+    args[where][bad].view(-1)[3 if where in ("v", "k") else 0] = value
+    out, fin = scan(args, S0)
+    torch.cuda.synchronize()
+    same = lambda a, c: torch.allclose(a.float(), c.float(), rtol=2 ** -7, atol=1e-3)
+    assert torch.isfinite(out[:bad]).all() and same(out[:bad], clean[:bad])
+    assert torch.isfinite(out[:, 1]).all() and same(out[:, 1], clean[:, 1]) and same(fin[0, 1], cfin[0, 1])
+    if where == "v":
+        ok = torch.arange(dv, device=DEV) != 3
+        assert torch.isfinite(out[:, 0, ok]).all() and same(out[:, 0, ok], clean[:, 0, ok])
+        assert same(fin[0, 0, ok], cfin[0, 0, ok])
+        assert not torch.isfinite(out[bad:, 0, 3]).any() and not torch.isfinite(fin[0, 0, 3]).any()
+    elif value == 0.0:
+        o, f = scan(args, None, bad)
+        torch.cuda.synchronize()
+        assert same(out[bad:, 0], o[:, 0]) and torch.allclose(fin[0, 0], f[0, 0], rtol=1e-5, atol=1e-6)
+    else:
+        assert not torch.isfinite(out[bad:, 0]).any() and not torch.isfinite(fin[0, 0]).any()
+    qs.close()
