@@ -94,10 +94,10 @@ struct ScanArgs {
 };
 
 // Segments of the scans: cells of `seg` tokens of the packed axis,
-// cut again where sequences begin; `count` bounds their number.  Delta rule in
-// chunks: seg is a chunk's 64 tokens, states its prepared matrices; sequences
-// of more than two cells of `cut` tokens (0: none) are cut, total has for each
-// piece L and M, [dv + dk][dk] a head.
+// cut again where sequences begin; `count` bounds their number.  Delta rule:
+// sequences of more than two cells of `cut` tokens (0: none) are cut, total has
+// for each piece L and M, [dv + dk][dk] a head; in chunks, seg is a chunk's 64
+// tokens and states its prepared matrices.
 struct ScanSegs {
   int32_t seg, count, cut;
   float* states;           // [count][H][dv][dk], null: no sequence is cut; delta rule: [count][H] kScanPrepBytes
@@ -106,6 +106,7 @@ struct ScanSegs {
 constexpr int kScanPrepBytes = 1024 + 18 * 1024 + 12 * 1024;
 hipError_t launch_scan_key(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
+hipError_t launch_delta_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan(const ScanArgs& a, const ScanSegs& g, hipStream_t s);
 hipError_t launch_scan_chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s);

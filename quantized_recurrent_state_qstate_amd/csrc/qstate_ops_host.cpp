@@ -230,6 +230,11 @@ struct ScanPlan {
   qs::ScanSegs segs;
   uint64_t states, total;   // workspace bytes
 };
+// Sequences of more than 2 cut tokens in pieces (delta rule).
+static void set_pieces(const qs::ScanArgs& a, int64_t cut, ScanPlan* p) {
+  p->segs.cut = (int32_t)cut;
+  p->total = (uint64_t)((a.T - 1) / cut + a.n) * (uint64_t)a.H * (uint64_t)(a.dv + a.dk) * (uint64_t)a.dk * 4u;
+}
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
   // sequences' average length: below 16 tokens (delta rule: 48, for its first
@@ -237,7 +242,17 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= (int64_t)a.n * (a.delta ? 48 : 16);
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
-  if (a.delta && !p.chunked) return p;
+  if (a.delta && !p.chunked) {
+    const int64_t rows = (int64_t)a.H * (a.dv + a.dk);   // of one piece's L and M
+    // Pieces: with up to 16384 rows at once a token costs little more than with
+    // few; of 64 tokens or more (dk 256: 128), and at least four, as they go
+    // twice.  fp32, one sequence: 1280 tokens of a head of 64 x 64 39 us, in one
+    // piece 196 (pieces of 128: 45); 5120 of 8 heads of 128 x 128 292, 944; 1280
+    // of 16 heads of 128 x 128 141, 239.
+    const int64_t cut = std::max<int64_t>(std::max(64, a.dk / 2), (a.T * rows / 16384 + 15) / 16 * 16);
+    if (4 * rows <= 16384 && (int64_t)a.n * a.H * a.dv <= 16384 && a.T > 2 * cut) set_pieces(a, cut, &p);
+    return p;
+  }
   if (a.delta) {
     p.segs.seg = 64;
     p.segs.count = (a.T + 63) / 64 + a.n;
@@ -247,13 +262,10 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     // heads of 256 x 256, 2048 tokens: 210 us with 512, 187 in one piece).  One
     // sequence of 8192 tokens: 2 heads of 128 x 128 105 us, in one piece 449; 8
     // heads 146, 461; 32 heads 336, 513.  A batch with none that is long pays
-    // for launches that do nothing (8 of 1024 tokens, 16 heads: 106 us, 98).
+    // for launches that do nothing (8 of 1024 tokens, 16 heads: 103 us, 98).
     const int64_t wide = (a.dv + 63) / 64, blocks = (int64_t)a.H * (wide + a.dk / 64);   // of one piece's L and M
     const int64_t cut = std::max<int64_t>(std::max(512, 4 * a.dk), (a.T / (256 / blocks + 1) + 63) / 64 * 64);
-    if (blocks <= 128 && a.n * a.H * wide <= 256 && a.T > 2 * cut) {
-      p.segs.cut = (int32_t)cut;
-      p.total = (uint64_t)((a.T + cut - 1) / cut + a.n) * (uint64_t)a.H * (uint64_t)(a.dv + a.dk) * (uint64_t)a.dk * 4u;
-    }
+    if (blocks <= 128 && a.n * a.H * wide <= 256 && a.T > 2 * cut) set_pieces(a, cut, &p);
     return p;
   }
   const int columns = p.chunked ? 64 : 32;     // a workgroup's
@@ -318,7 +330,7 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
     if (overlap(w, fin) || overlap(w, ini) || overlap(w, out))
       return op_fail(QS_EINVAL, "the workspace overlaps an output or the initial state");
     p.segs.total = (float*)workspace;
-    p.segs.states = (float*)((char*)workspace + p.total);
+    if (p.states) p.segs.states = (float*)((char*)workspace + p.total);
   }
   if ((int64_t)p.segs.count * a.H * ((a.dv + 31) / 32) > 0x7FFFFFFF ||
       (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > 0x7FFFFFFF)

@@ -12,10 +12,13 @@
 //
 // It carries fp32 prompts, short ones, and the delta rule with a decay a
 // channel.  Bound by the chain from token to token (a reduction in it by the
-// delta rule, which cannot be cut): about 0.19 us a token, 378 us for 2048
-// tokens of 8 heads of 64 x 64.  Additive sequences are cut into segments: one
-// pass for the states that the segments add (no queries, no outputs), the join,
-// one pass for the outputs; 53 us against 464 us uncut for the same sizes.
+// delta rule): about 0.19 us a token, 378 us for 2048 tokens of 8 heads of
+// 64 x 64 in one piece.  So long sequences are cut.  Additive: one pass for the
+// states that the segments add (no queries, no outputs), the join, one pass for
+// the outputs; 53 us against 464 uncut for the same sizes.  Delta rule, of few
+// heads: the first pass makes L and M of each piece, which maps the state before
+// it to S M + L (M's rows: the state's of an identity with values of zero);
+// 5120 tokens of 8 heads of 64 x 64: 119 us against 779.
 #include <hip/hip_runtime.h>
 
 #include "qstate_scan_tiles.hpp"
@@ -78,22 +81,32 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
   __shared__ float sk[kStage][DK], sq[OUT ? kStage : 1][OUT ? DK : 1], sd[KEY ? kStage : 1][KEY ? DK : 1];
   __shared__ float sv[kStage][kRows], so[OUT ? kStage : 1][OUT ? kRows : 1], sg[kStage], sb[kStage];
   const int tid = (int)threadIdx.x;
-  const int per = a.H * rchunks;
+  const int per = a.H * (DELTA && !OUT ? rchunks + DK / kRows : rchunks);
   const int sid = (int)(blockIdx.x / (uint32_t)per), hr = (int)(blockIdx.x % (uint32_t)per);
-  const int h = hr / rchunks, rc = hr % rchunks;
+  const int h = hr / (per / a.H), rc = hr % (per / a.H);
   const int g = h / (a.H / a.G);
-  const Segment seg = find_segment(a, gs.seg, sid);
-  if (seg.none || (!OUT && seg.last)) return;
+  Piece seg;
+  if constexpr (DELTA) {
+    seg = find_piece(a, gs.cut, sid);
+  } else {
+    const Segment x = find_segment(a, gs.seg, sid);
+    seg = {x.seq, x.t0, x.t1, x.first, x.last, x.none};
+  }
+  const bool matrix = DELTA && !OUT && rc >= rchunks;   // rows of M
+  if (seg.none || (!OUT && (seg.last || (matrix && seg.first)))) return;
   const int t0 = seg.t0, t1 = seg.t1;
   const int sub = tid & 15, row = (tid >> 4) * RPL;   // this lane's channels and first row
-  const int r0 = rc * kRows;
-  const int64_t st = (int64_t)h * a.dv, states = (int64_t)a.H * a.dv * DK;
+  const int r0 = (matrix ? rc - rchunks : rc) * kRows, rows = matrix ? DK : a.dv;
   // a sequence in one piece begins with its own state; of several pieces all
   // states are kept in the workspace (final may be initial)
-  const float* from = !OUT ? nullptr
-                      : seg.first && seg.last ? (a.initial ? a.initial + seg.seq * states : nullptr)
-                                              : gs.states + sid * states;
-  float* to = !OUT ? gs.states + sid * states : seg.last ? a.final + seg.seq * states : nullptr;
+  const int64_t own = ((int64_t)seg.seq * a.H + h) * a.dv * DK;
+  float* kept = DELTA ? gs.total + (((int64_t)sid * a.H + h) * (a.dv + DK) + (matrix ? a.dv : 0)) * DK
+                      : gs.states + ((int64_t)sid * a.H + h) * a.dv * DK;
+  const bool whole = seg.first && seg.last;
+  const float* from = OUT && !whole                                    ? kept
+                      : (OUT || DELTA) && seg.first && a.initial ? a.initial + own
+                                                                       : nullptr;
+  float* to = !OUT ? kept : seg.last ? a.final + own : nullptr;
 
   float s[RPL][kM][4];
 #pragma unroll
@@ -101,9 +114,12 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
       float4 x = make_float4(0, 0, 0, 0);
-      if (from && r0 + row + r < a.dv)
-        x = *(const float4*)(from + (st + r0 + row + r) * DK + m * 64 + sub * 4);
+      if (from && !matrix && r0 + row + r < rows)
+        x = *(const float4*)(from + (int64_t)(r0 + row + r) * DK + m * 64 + sub * 4);
       s[r][m][0] = x.x; s[r][m][1] = x.y; s[r][m][2] = x.z; s[r][m][3] = x.w;
+      if (matrix)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[r][m][e] = m * 64 + sub * 4 + e == r0 + row + r ? 1.0f : 0.0f;
     }
 
   // what this thread brings of a stage: token bt, channels bc..; v: rows of token vt
@@ -128,7 +144,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       const int e = tid * kV + j, vt = e / kRows, vr = e % kRows;
-      nv[j] = (t + vt < t1 && r0 + vr < a.dv) ? get1<BF16>(a.v, (int64_t)(t + vt) * a.vs + (int64_t)h * a.dv + r0 + vr)
+      nv[j] = (!matrix && t + vt < t1 && r0 + vr < rows) ? get1<BF16>(a.v, (int64_t)(t + vt) * a.vs + (int64_t)h * a.dv + r0 + vr)
                                               : 0.0f;
     }
     ng = nb = 1.0f;
@@ -138,7 +154,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
     }
   };
 
-  float all[KEY ? kM : 1][4];
+  [[maybe_unused]] float all[KEY ? kM : 1][4];
 #pragma unroll
   for (int m = 0; m < (KEY ? kM : 1); ++m)
 #pragma unroll
@@ -206,7 +222,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
 #pragma unroll
         for (int r = 0; r < RPL; ++r)
           if (sub == r) so[i][row + r] = o[r];
-      if constexpr (!OUT) {                  // the segment's whole decay
+      if constexpr (!OUT && !DELTA) {        // the segment's whole decay
         if constexpr (KEY) {
 #pragma unroll
           for (int m = 0; m < kM; ++m)
@@ -244,12 +260,12 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
   if (to)
 #pragma unroll
     for (int r = 0; r < RPL; ++r)
-      if (r0 + row + r < a.dv)
+      if (r0 + row + r < rows)
 #pragma unroll
         for (int m = 0; m < kM; ++m)
-          *(float4*)(to + (st + r0 + row + r) * DK + m * 64 + sub * 4) =
+          *(float4*)(to + (int64_t)(r0 + row + r) * DK + m * 64 + sub * 4) =
               make_float4(s[r][m][0], s[r][m][1], s[r][m][2], s[r][m][3]);
-  if (!OUT && rc == 0 && tid < 16) {
+  if (!OUT && !DELTA && rc == 0 && tid < 16) {
     if constexpr (KEY) {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
@@ -264,8 +280,16 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
 template <int BF16, int DK, bool DELTA, bool KEY, int RPL>
 hipError_t scan_rows(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int rchunks = (a.dv + 16 * RPL - 1) / (16 * RPL);
-  const uint32_t grid = (uint32_t)(g.count * a.H * rchunks);
-  if constexpr (!DELTA) {
+  const int pieces = !DELTA ? g.count : a.n + (g.cut > 0 ? (a.T - 1) / g.cut : 0);
+  const uint32_t grid = (uint32_t)(pieces * a.H * rchunks);
+  if constexpr (DELTA) {
+    if (g.cut > 0) {
+      const uint32_t both = (uint32_t)(pieces * a.H * (rchunks + DK / (16 * RPL)));
+      k_scan<BF16, DK, DELTA, KEY, RPL, false><<<dim3(both), 256, 0, s>>>(a, g, rchunks);
+      const hipError_t e = launch_delta_join(a, g, s);
+      if (e != hipSuccess) return e;
+    }
+  } else {
     if (g.states) {
       k_scan<BF16, DK, DELTA, KEY, RPL, false><<<dim3(grid), 256, 0, s>>>(a, g, rchunks);
       const hipError_t e = launch_scan_join(a, g, s);

@@ -204,23 +204,6 @@ struct Chunk {
   float prep[kPrepFloats];
 };
 
-// A piece of a sequence: of one of more than two cells the part in cell c, of any
-// other all of it.  Whether a sequence is cut depends on its offsets, which
-// the host does not know: a short one gains nothing.
-struct Piece {
-  int seq, t0, t1, cell;
-  bool first, last, none;
-};
-__device__ __forceinline__ bool long_enough(int start, int end, int cut) { return cut > 0 && (end - start + 1) / 2 > cut; }
-__device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
-  Segment g{s, 0, 0, true, true, false};
-  if (cut > 0) g = find_segment(a, cut, s);
-  const int start = a.offsets ? min(max(a.offsets[g.seq], 0), a.T) : 0;
-  const int end = a.offsets ? min(max(a.offsets[g.seq + 1], start), a.T) : a.T;
-  if (long_enough(start, end, cut)) return {g.seq, g.t0, g.t1, s, g.first, g.last, g.none};
-  return {g.seq, start, end, s, true, true, g.none || !g.first};
-}
-
 // A sequence's chunks in order; a workgroup holds 16 WAVES value columns of a
 // head, each wave 16 in accumulators [dk][v] (rows dealt so that a lane holds 8
 // channels in a row, the second operand of S k and S q as it is).  While a
@@ -245,7 +228,8 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   const int m = lane & 15, q4 = lane >> 4;
   const int per = a.H * (OUT ? vchunks : vchunks + DK / kDV);
   const int hv = (int)(blockIdx.x % (uint32_t)per), h = hv % a.H, kh = h / (a.H / a.G);
-  const Piece piece_of = find_piece(a, cut, (int)(blockIdx.x / (uint32_t)per));
+  const int part = (int)(blockIdx.x / (uint32_t)per);
+  const Piece piece_of = find_piece(a, cut, part);
   const bool matrix = !OUT && hv / a.H >= vchunks;   // columns of M
   const int v0 = matrix ? 0 : hv / a.H * kDV, m0 = matrix ? (hv / a.H - vchunks) * kDV : 0;
   if (piece_of.none || (!OUT && (piece_of.last || (matrix && piece_of.first)))) return;
@@ -256,7 +240,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   // this lane's row of the states given and kept, channels 8 q4 .. of every 32
   const int64_t at_state = (st + head + v) * DK + 8 * q4;
   const int64_t at_carry =
-      (((int64_t)piece_of.cell * a.H + h) * (a.dv + DK) + (matrix ? a.dv + m0 + col : v)) * DK + 8 * q4;
+      (((int64_t)part * a.H + h) * (a.dv + DK) + (matrix ? a.dv + m0 + col : v)) * DK + 8 * q4;
   const bool real = matrix || v < a.dv;
   const float* from = OUT && !(piece_of.first && piece_of.last) ? carry + at_carry
                       : piece_of.first && a.initial             ? a.initial + at_state
@@ -535,7 +519,7 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, f
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
   if (!long_enough(start, end, cut)) return;
   const int c0 = start / cut, c1 = (end - 1) / cut;
-  auto piece_at = [&](int c) { return carry + ((int64_t)(c + seq) * a.H + h) * (a.dv + DK) * DK; };
+  auto piece_at = [&](int c) { return carry + ((int64_t)(c == c0 ? seq : a.n + c - 1) * a.H + h) * (a.dv + DK) * DK; };
   // this thread's elements of the rows, tid + 512 e, and its part of M: a channel, kJ rows
   const int ch = tid % DK, j0 = tid / DK * kJ;
   const int rows = min(kJoinRows, a.dv - r0) * DK;   // elements there are
@@ -600,6 +584,13 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, f
   for (int e = 0; e < kE; ++e) keep(c1, e, S[e]);
 }
 
+template <int DK>
+hipError_t join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  const int rchunks = (a.dv + kJoinRows - 1) / kJoinRows;
+  k_delta_join<DK><<<dim3((uint32_t)(a.n * a.H * rchunks)), 512, 0, s>>>(a, g.cut, g.total, rchunks);
+  return hipGetLastError();
+}
+
 template <int DK, bool VEC>
 hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   // 64 columns a workgroup: with 32, twice as many workgroups bring the same
@@ -608,12 +599,12 @@ hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
   k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
-  const int pieces = g.cut > 0 ? (a.T + g.cut - 1) / g.cut + a.n : a.n;
+  const int pieces = a.n + (g.cut > 0 ? (a.T - 1) / g.cut : 0);
   if (g.cut > 0) {
-    const int rchunks = (a.dv + kJoinRows - 1) / kJoinRows;
     k_delta_scan<DK, WAVES, VEC, false><<<dim3((uint32_t)(pieces * a.H * (vchunks + DK / (16 * WAVES)))), 64 * WAVES, 0, s>>>(
         a, g.states, g.cut, g.total, vchunks);
-    k_delta_join<DK><<<dim3((uint32_t)(a.n * a.H * rchunks)), 512, 0, s>>>(a, g.cut, g.total, rchunks);
+    const hipError_t e = join<DK>(a, g, s);
+    if (e != hipSuccess) return e;
   }
   k_delta_scan<DK, WAVES, VEC, true><<<dim3((uint32_t)(pieces * a.H * vchunks)), 64 * WAVES, 0, s>>>(
       a, g.states, g.cut, g.total, vchunks);
@@ -626,6 +617,10 @@ hipError_t delta_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_delta_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
+  return a.dk == 64 ? join<64>(a, g, s) : a.dk == 128 ? join<128>(a, g, s) : join<256>(a, g, s);
+}
 
 hipError_t launch_scan_delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   return a.dk == 64 ? delta_dk<64>(a, g, s) : a.dk == 128 ? delta_dk<128>(a, g, s) : delta_dk<256>(a, g, s);

@@ -90,21 +90,25 @@ struct Segment {
   int seq, t0, t1;      // tokens
   bool first, last, none;
 };
+// The last sequence i > 0 with `le(i)`, which holds up to some i and not behind; else 0.
+template <class F>
+__device__ __forceinline__ int last_sequence(const ScanArgs& a, F le) {
+  const int lane = (int)(threadIdx.x & 63u);
+  int lo = 0, len = a.n - 1;
+  while (len > 0) {
+    const int step = (len + 63) >> 6;
+    const int i = lo + (lane + 1) * step;
+    const int c = (int)__popcll(__ballot(i <= lo + len && le(i)));
+    lo += c * step;
+    len = min(len - c * step, step - 1);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
 __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int s) {
   Segment r{0, 0, 0, true, true, false};
   int start = 0, end = a.T;
   if (a.offsets) {
-    const int lane = (int)(threadIdx.x & 63u);
-    int lo = 0, len = a.n - 1;              // sequences i in [1, n-1] with offsets[i] / seg + i <= s
-    while (len > 0) {
-      const int step = (len + 63) >> 6;
-      const int i = lo + (lane + 1) * step;
-      const bool le = i <= lo + len && min(max(a.offsets[i], 0), a.T) / seg + i <= s;
-      const int c = (int)__popcll(__ballot(le));
-      lo += c * step;
-      len = min(len - c * step, step - 1);
-    }
-    r.seq = __builtin_amdgcn_readfirstlane(lo);
+    r.seq = last_sequence(a, [&](int i) { return min(max(a.offsets[i], 0), a.T) / seg + i <= s; });
     start = min(max(a.offsets[r.seq], 0), a.T);
     end = min(max(a.offsets[r.seq + 1], start), a.T);
   }
@@ -115,6 +119,29 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
   r.t0 = r.first ? start : c * seg;
   r.t1 = r.last ? end : (c + 1) * seg;
   return r;
+}
+
+// Piece s of the delta rule's scans.  A sequence of more than two cells of `cut`
+// tokens (of the packed axis) is cut where cells begin, any other is one piece:
+// whether it is depends on the offsets, which the host does not know.  Piece
+// s < n is the first of sequence s, piece n + c - 1 the one from cell c on, if
+// cell c begins inside a sequence that is cut: what there may be none of comes
+// last in a grid, or it leaves the rest badly dealt to the compute units (4
+// sequences of 512 tokens of 16 heads token by token: 127 us, 179 with
+// find_segment's order, 121 with no pieces).
+struct Piece {
+  int seq, t0, t1;
+  bool first, last, none;
+};
+__device__ __forceinline__ bool long_enough(int start, int end, int cut) { return cut > 0 && (end - start + 1) / 2 > cut; }
+__device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
+  const int x = s < a.n ? 0 : (s - a.n + 1) * cut;
+  const int seq = s < a.n ? s : a.offsets ? last_sequence(a, [&](int i) { return a.offsets[i] <= x; }) : 0;
+  const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
+  const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
+  const bool many = long_enough(start, end, cut);
+  if (s < a.n) return {seq, start, many ? (start / cut + 1) * cut : end, true, !many, false};
+  return {seq, x, min(x + cut, end), false, x + cut >= end, !(many && start < x && x < end)};
 }
 
 // 16 bytes a lane from a buffer at `offset` to LDS, lane after lane from `to` on

@@ -125,7 +125,8 @@ int main() {
         CHECK(qstate_scan(h, &a, ws, need, nullptr) == QS_OK);
         const bool chunked = dtype == QS_BF16 && !(kind == QS_KIND_DELTA && decay == QS_DECAY_KEY);
         CHECK((g_chunked != 0) == chunked);
-        CHECK((need > 0) == (chunked || kind == QS_KIND_ADDITIVE) && (need > 0) == (g_segs.states != nullptr));
+        CHECK(need > 0 && (kind == QS_KIND_ADDITIVE || chunked) == (g_segs.states != nullptr));
+        CHECK((g_segs.cut > 0) == (kind == QS_KIND_DELTA));
         if (need) {
           CHECK(qstate_scan(h, &a, nullptr, need, nullptr) == QS_EINVAL);
           CHECK(qstate_scan(h, &a, ws + 16, need, nullptr) == QS_EINVAL);
@@ -208,6 +209,11 @@ int main() {
             if (g_segs.states) {
               const uint64_t per = g_chunked == 3 ? (uint64_t)qs::kScanPrepBytes : 64ull * 128 * 4;
               CHECK((char*)g_segs.states + (uint64_t)g_segs.count * 8 * per <= at(6000ull << 32) + need);
+            }
+            if (g_segs.cut > 0) {                     // pieces: L and M in front of the prepared chunks
+              const uint64_t pieces = (uint64_t)((T - 1) / g_segs.cut + n);
+              CHECK((char*)g_segs.total + pieces * 8 * (64 + 128) * 128 * 4 <=
+                    (g_segs.states ? (char*)g_segs.states : at(6000ull << 32) + need));
             }
           }
         }

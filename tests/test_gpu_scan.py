@@ -362,20 +362,32 @@ def test_scan_delta_in_pieces(lengths, dk, dv, H):
     run("delta", "head", lengths, H, 1, dk, dv, "bf16", mu=2.0)
 
 
+@pytest.mark.parametrize("dtype,decay", [("fp32", "head"), ("fp32", "key"), ("bf16", "key")])
+@pytest.mark.parametrize("lengths", [[193], [128, 129], [3, 150, 0, 400], [200, 200, 200], [15, 513, 1, 128]])
+@pytest.mark.parametrize("dk,dv,H", [(64, 64, 4), (128, 33, 2), (256, 24, 2), (64, 100, 16)])
+def test_scan_delta_in_pieces_token_by_token(dtype, decay, lengths, dk, dv, H):
+    run("delta", decay, lengths, H, 2, dk, dv, dtype, initial=True, skip=True, strided=True, mu=5.0)
+    run("delta", decay, lengths, H, 1, dk, dv, dtype, mu=2.0)
+
+
 @pytest.mark.parametrize("where,value", [("v", float("nan")), ("v", float("inf")), ("k", float("nan")),
                                          ("decay", float("nan")), ("decay", 0.0), ("beta", float("inf"))])
-def test_scan_delta_in_pieces_odd_values(where, value):
+@pytest.mark.parametrize("dtype,decay", [("bf16", "head"), ("fp32", "head"), ("bf16", "key")])
+def test_scan_delta_in_pieces_odd_values(where, value, dtype, decay):
     """As in a sequence in one piece: a value that is not finite reaches its head (v: its row) from its token on, and a
     decay of zero cuts off what was before."""
     T, bad, H, dv = 2600, 1300, 2, 48
     names = ("q", "k", "v", "decay", "beta")
-    args = dict(zip(names, (x.to(DEV) for x in inputs("delta", "head", [T], H, 2, 64, dv, "bf16", mu=6.0))))
-    qs = QState(StateConfig(kind="delta", decay_mode="head", B=1, H=H, dk=64, dv=dv))
+    args = dict(zip(names, (x.to(DEV) for x in inputs("delta", decay, [T], H, 2, 64, dv, dtype, mu=6.0))))
+    qs = QState(StateConfig(kind="delta", decay_mode=decay, B=1, H=H, dk=64, dv=dv, in_dtype=dtype))
     S0 = torch.randn(1, H, dv, 64, device=DEV)
     scan = lambda a, S, t0=0: qs.scan(*(a[n][t0:] for n in names), initial=S)
     clean, cfin = scan(args, S0)
     args[where] = args[where].clone()
-    args[where][bad].view(-1)[3 if where in ("v", "k") else 0] = value
+    if where == "decay":
+        args[where][bad].view(H, -1)[0] = value
+    else:
+        args[where][bad].view(-1)[3 if where in ("v", "k") else 0] = value
     out, fin = scan(args, S0)
     torch.cuda.synchronize()
     same = lambda a, c: torch.allclose(a.float(), c.float(), rtol=2 ** -7, atol=1e-3)
