@@ -98,16 +98,25 @@ def _state_dtypes(cfg: "StateConfig") -> dict:
 _ITEM = {"uint8": 1, "bfloat16": 2, "float32": 4, "int32": 4}
 
 
+_Tensor: tuple | type = ()          # torch.Tensor, once a check has imported torch
+
+
+def _tensor_type() -> None:
+    global _Tensor
+    import torch
+    _Tensor = torch.Tensor
+
+
 def check_tensor(name: str, t, dtype, numel: int, device, at_least: bool = False) -> None:
     """Host-side argument check before a pointer crosses the C ABI: the kernels
     read and write exactly the planned extents, so a tensor of the wrong dtype,
     size, memory layout or device would make them read or write out of bounds
     or get wrong results.  Raises ValueError (checks in that order)."""
-    import torch
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
             and (t.numel() == numel or (at_least and t.numel() > numel))):
         return
-    if not isinstance(t, torch.Tensor):
+    _tensor_type()
+    if not isinstance(t, _Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -148,11 +157,10 @@ def check_inputs(cfg: "StateConfig", n: int, device, q, k, v, decay, beta, out) 
 def check_rows(name: str, t, dtype, shape, device) -> int:
     """A tensor of `shape` whose rows (all dimensions but the first) are
     contiguous, at any stride between them; returns that stride in elements."""
-    import torch
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return t.stride(0) if shape[0] > 1 else t.numel()
-    if not isinstance(t, torch.Tensor):
+    _tensor_type()
+    if not isinstance(t, _Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")

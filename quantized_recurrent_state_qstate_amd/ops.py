@@ -27,7 +27,7 @@ def _call(fn, name: str, args, device, stream) -> None:
         raise ValueError(f"{name}: tensors on {device}, expected a GPU")
     if stream is not None and stream.device != device:
         raise ValueError(f"stream on {stream.device}, expected {device}")
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         _lib.check(fn(ctypes.byref(args), raw_stream(stream, device)), name)
     else:
         with torch.cuda.device(device):
