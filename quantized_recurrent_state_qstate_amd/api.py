@@ -157,15 +157,17 @@ def check_inputs(cfg: "StateConfig", n: int, device, q, k, v, decay, beta, out) 
 def check_rows(name: str, t, dtype, shape, device) -> int:
     """A tensor of `shape` whose rows (all dimensions but the first) are
     contiguous, at any stride between them; returns that stride in elements."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return t.stride(0) if shape[0] > 1 else t.numel()
-    _tensor_type()
-    if not isinstance(t, _Tensor):
-        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
+        if t.is_contiguous():
+            return t.stride(0) if shape[0] > 1 else t.numel()
+    else:
+        _tensor_type()
+        if not isinstance(t, _Tensor):
+            raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
     if len(st) == 3 and st[2] == 1 and st[1] == shape[2]:
         width = shape[1] * shape[2]
@@ -194,6 +196,16 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(x, contiguous: bool, stream):
+    """`_empty` of x's shape, dtype and device."""
+    if stream is not None:
+        return _empty(x.shape, x.dtype, x.device, stream)
+    if not contiguous:
+        return x.new_empty(x.shape)
+    import torch
+    return torch.empty_like(x)
+
+
 def raw_stream(stream, device) -> int:
     """The hipStream_t of `stream`, or of the device's current stream."""
     if stream is not None:
@@ -215,6 +227,9 @@ class QState:
                    "qstate_init")
         self.sizes = {n: int(getattr(s, n)) for n, _ in _lib.Sizes._fields_}
         self.device = torch.device("cuda", torch.cuda.current_device())
+        # the planned buffers: name, what errors call it, dtype, elements
+        self._buffers = [(n, f"state[{n!r}]", getattr(torch, dt), self.sizes[n] // _ITEM[dt])
+                         for n, dt in _state_dtypes(cfg).items() if self.sizes[n]]
         self._scan_bytes = {}     # workspace sizes by (tokens, sequences, key heads)
 
     def close(self) -> None:
@@ -354,7 +369,7 @@ class QState:
         if initial is not None:
             check_tensor("initial", initial, f32, n * H * dv * dk, dev)
         if out is None:
-            out = _empty((T, H, dv), ind, dev, stream)
+            out = _empty_like(v, vs == H * dv, stream)
             os = H * dv
         else:
             os = check_rows("out", out, ind, (T, H, dv), dev)
@@ -379,11 +394,12 @@ class QState:
 
     def _checked(self, st: dict, slots: int) -> _lib.Tensors:
         """The buffers of a state of `slots` slots, checked, as the C ABI takes them."""
-        B = self.cfg.B
-        check_state(self.cfg, self.sizes if slots == B else {n: z // B * slots if B else 0 for n, z in self.sizes.items()},
-                    st, self.device)
-        ptrs = [st.get(n) for n in _lib.TENSORS]
-        return _lib.Tensors(*[x.data_ptr() if x is not None and x.numel() > 0 else None for x in ptrs])
+        B, t = self.cfg.B, _lib.Tensors()
+        for name, label, dtype, numel in self._buffers:
+            x = st.get(name)
+            check_tensor(label, x, dtype, numel if slots == B else numel // B * slots, self.device, at_least=True)
+            setattr(t, name, x.data_ptr())
+        return t
 
     def _extra(self, extra, source_extra, src_slots: int):
         """Per-slot buffers that go along: tensors [slots, ...], contiguous, on this device."""

@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .api import _empty, _ptr, check_rows, check_tensor, raw_stream
+from .api import _empty_like, _ptr, check_rows, check_tensor, raw_stream
 
 
 def _device(name: str, x):
@@ -22,13 +22,15 @@ def _device(name: str, x):
 
 def _call(fn, name: str, args, device, stream) -> None:
     """Launch on `stream` (None: the device's current one) with the tensors' device current."""
-    import torch
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors on {device}, expected a GPU")
     if stream is not None and stream.device != device:
         raise ValueError(f"stream on {stream.device}, expected {device}")
+    import torch
     if device.index == torch._C._cuda_getDevice():
-        _lib.check(fn(ctypes.byref(args), raw_stream(stream, device)), name)
+        status = fn(ctypes.byref(args), raw_stream(stream, device))
+        if status:
+            _lib.check(status, name)
     else:
         with torch.cuda.device(device):
             _lib.check(fn(ctypes.byref(args), raw_stream(stream, device)), name)
@@ -53,7 +55,7 @@ def _conv(x, weight, bias, window, slot, n, silu, out, stream):
     if slot is not None:
         check_tensor("slot", slot, torch.int32, n, dev)
     if out is None:
-        out = _empty((T, C), dtype, dev, stream)
+        out = _empty_like(x, xs == C, stream)
         os = C
     else:
         os = check_rows("out", out, dtype, (T, C), dev)
@@ -117,7 +119,7 @@ def qk_norm_rotate(q, k=None, *, norm="l2", q_weight=None, k_weight=None, eps=1e
     ks = kos = hq * d
     qs = check_rows("q", q, dtype, (T, hq, d), dev)
     if q_out is None:
-        q_out = _empty((T, hq, d), dtype, dev, stream)
+        q_out = _empty_like(q, qs == hq * d, stream)
         qos = hq * d
     else:
         qos = check_rows("q_out", q_out, dtype, (T, hq, d), dev)
@@ -125,7 +127,7 @@ def qk_norm_rotate(q, k=None, *, norm="l2", q_weight=None, k_weight=None, eps=1e
         hk = k.shape[1]
         ks = check_rows("k", k, dtype, (T, hk, d), dev)
         if k_out is None:
-            k_out = _empty((T, hk, d), dtype, dev, stream)
+            k_out = _empty_like(k, ks == hk * d, stream)
             kos = hk * d
         else:
             kos = check_rows("k_out", k_out, dtype, (T, hk, d), dev)
