@@ -248,9 +248,10 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     // few; of 64 tokens or more (dk 256: 128), and at least four, as they go
     // twice.  fp32, one sequence: 1280 tokens of a head of 64 x 64 39 us, in one
     // piece 196 (pieces of 128: 45); 5120 of 8 heads of 128 x 128 292, 944; 1280
-    // of 16 heads of 128 x 128 141, 239.
+    // of 16 heads of 128 x 128 141, 239.  Every sequence has a place for L and M,
+    // so not with many (32768 rows of 256 are 34 MB).
     const int64_t cut = std::max<int64_t>(std::max(64, a.dk / 2), (a.T * rows / 16384 + 15) / 16 * 16);
-    if (4 * rows <= 16384 && (int64_t)a.n * a.H * a.dv <= 16384 && a.T > 2 * cut) set_pieces(a, cut, &p);
+    if (4 * rows <= 16384 && a.n * rows <= 32768 && a.T > 2 * cut) set_pieces(a, cut, &p);
     return p;
   }
   if (a.delta) {
