@@ -90,7 +90,7 @@ struct ScanArgs {
   int64_t qs, ks, vs, ds, bs, os;   // elements between tokens
   int32_t T, n, H, G, dk, dv;
   int32_t bf16, delta, key;
-  int32_t vec;             // q, k, v and out rows allow 16-byte accesses
+  int32_t vec;             // 16-byte accesses: 2 to q, k, v and out rows, 1 to q and k, 0 to none
 };
 
 // Segments of the scans: cells of `seg` tokens of the packed axis,

@@ -36,8 +36,8 @@
 namespace qs {
 namespace {
 
-template <int DK, int NV, int WAVES, bool OUT, bool VEC>
-__global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
+template <int DK, int NV, int WAVES, bool OUT, int VEC>
+__global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_chunk(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kT = 64 * WAVES;            // threads
   constexpr int kDV = 16 * NV * WAVES;      // value columns
   constexpr int kKS = DK / 32;              // steps of 32 channels
@@ -85,9 +85,9 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
   float nd = 1.0f, nb = 0.0f;
   auto fetch = [&](int t, int t1) {
     const int rows = min(kL, t1 - t);
-    const Tile<VEC> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
-    const Tile<VEC> tq(OUT ? a.q : a.k, OUT ? (int64_t)t * a.qs + (int64_t)kh * DK : 0, a.qs, rows, DK);
-    const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
+    const Tile<(VEC > 0)> tk(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK);
+    const Tile<(VEC > 0)> tq(OUT ? a.q : a.k, OUT ? (int64_t)t * a.qs + (int64_t)kh * DK : 0, a.qs, rows, DK);
+    const Tile<VEC == 2> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, rows, min(kDV, a.dv - v0));
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
       nk[i] = tk.load_step(kr, kc, i, kKStep);
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC ? 2 : 1) void k_scan_c
     }
     if constexpr (OUT) {
       __syncthreads();                       // outputs are in LDS, the chunk has been read
-      const Tile<VEC> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
+      const Tile<VEC == 2> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
 #pragma unroll
       for (int i = 0; i < kVP; ++i) to.store_step(vr, vc, i, kVStep, *(const U4*)&sv[vr * kVR + vc + i * (kVStep * kVR)]);
     }
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
   if (c1 > c0) st[(int64_t)(c1 + seq) * all + e] = S;
 }
 
-template <int DK, int NV, int WAVES, bool VEC>
+template <int DK, int NV, int WAVES, int VEC>
 hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int vchunks = (a.dv + 16 * NV * WAVES - 1) / (16 * NV * WAVES);
   const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
@@ -417,7 +417,7 @@ hipError_t chunk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 
 template <int DK>
 hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  return a.vec ? chunk<DK, 1, 4, true>(a, g, s) : chunk<DK, 1, 4, false>(a, g, s);
+  return a.vec == 2 ? chunk<DK, 1, 4, 2>(a, g, s) : a.vec ? chunk<DK, 1, 4, 1>(a, g, s) : chunk<DK, 1, 4, 0>(a, g, s);
 }
 
 }  // namespace

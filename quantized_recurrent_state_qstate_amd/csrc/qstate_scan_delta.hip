@@ -215,7 +215,7 @@ struct Chunk {
 // rows, from zero or the first piece's initial state) and M (further dk rows:
 // values of zero, from the identity) into `carry`, k_delta_join goes from
 // piece to piece, and the OUT pass makes the outputs of all pieces at once.
-template <int DK, int WAVES, bool VEC, bool OUT>
+template <int DK, int WAVES, int VEC, bool OUT>
 __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int cut, float* carry,
                                                               int vchunks) {
   constexpr int kDV = 16 * WAVES, kKS = DK / 32;
@@ -263,9 +263,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   constexpr int kPieces = kK + kQ + kV + kP;
   auto bringing = [&](Buf& b, int t, int t1) {   // piece i of the chunk from t to t1 into b
     const int rows = t1 - t;
-    return [&b, wave, lane, tk = Tile<VEC>(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK),
-            tq = Tile<VEC>(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK),
-            tv = Tile<VEC>(a.v, (int64_t)t * a.vs + head + v0, a.vs, matrix ? 0 : rows, min(kDV, a.dv - v0)),
+    return [&b, wave, lane, tk = Tile<(VEC > 0)>(a.k, (int64_t)t * a.ks + (int64_t)kh * DK, a.ks, rows, DK),
+            tq = Tile<(VEC > 0)>(a.q, (int64_t)t * a.qs + (int64_t)kh * DK, a.qs, rows, DK),
+            tv = Tile<VEC == 2>(a.v, (int64_t)t * a.vs + head + v0, a.vs, matrix ? 0 : rows, min(kDV, a.dv - v0)),
             tp = Tile<true>(prep, 2 * ((int64_t)(t / kL + seq) * a.H + h) * kPrepFloats, 0, min(rows, 1), kPrepFloats * 2)](
                int i) {
       if (i < kK) tk.template bring<DK>(b.k, (i * WAVES + wave) * 512, lane);
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       if (r < done_n) {
         const U4 y = *(const U4*)&so[wave][r * 16 + c];
         uint16_t* o = (uint16_t*)a.out + (int64_t)(done_t + r) * a.os + head + v0 + wave * 16 + c;
-        if constexpr (VEC) {
+        if constexpr (VEC == 2) {
           if (v0 + wave * 16 + c < a.dv) *(U4*)o = y;
         } else {
 #pragma unroll
@@ -591,14 +591,14 @@ hipError_t join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DK, bool VEC>
+template <int DK, int VEC>
 hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   // 64 columns a workgroup: with 32, twice as many workgroups bring the same
   // keys (one sequence of 7868 tokens, 32 heads of 128 x 128: 493 against 506 us
   // in all; sixteen of 256: 107, 172).
   constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
-  k_delta_prep<DK, VEC><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
+  k_delta_prep<DK, (VEC > 0)><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
   const int pieces = a.n + (g.cut > 0 ? (a.T - 1) / g.cut : 0);
   if (g.cut > 0) {
     k_delta_scan<DK, WAVES, VEC, false><<<dim3((uint32_t)(pieces * a.H * (vchunks + DK / (16 * WAVES)))), 64 * WAVES, 0, s>>>(
@@ -613,7 +613,7 @@ hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 
 template <int DK>
 hipError_t delta_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
-  return a.vec ? delta<DK, true>(a, g, s) : delta<DK, false>(a, g, s);
+  return a.vec == 2 ? delta<DK, 2>(a, g, s) : a.vec ? delta<DK, 1>(a, g, s) : delta<DK, 0>(a, g, s);
 }
 
 }  // namespace

@@ -72,8 +72,8 @@ __device__ __forceinline__ void put_piece(uint16_t* to, float (&f)[N], bool last
     for (int j = 0; j < N; ++j) f[j] -= cut(f[j]);
 }
 
-template <int DK, int NV, bool OUT, bool VEC>
-__global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(const ScanArgs a, const ScanSegs g, int vchunks) {
+template <int DK, int NV, bool OUT, int VEC>
+__global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kDV = 64 * NV, kKS = DK / 32, kC = DK / 64, kR = DK + 8, kVR = kDV + 8;
   constexpr int kVP = kB * kDV / 8;                                    // 16-byte pieces of v
   __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? 2 : 1][OUT ? kB * kR : 8];   // q D
@@ -127,13 +127,13 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
       if (tt < sg.t1) {
 #pragma unroll
         for (int j = 0; j < kC; ++j) nd[i][j] = a.decay[tt * a.ds + (int64_t)h * DK + ch + j];
-        get_bf16<kC, VEC>(a.k, tt * a.ks + (int64_t)kh * DK + ch, nk[i]);
-        if constexpr (OUT) get_bf16<kC, VEC>(a.q, tt * a.qs + (int64_t)kh * DK + ch, nq[i]);
+        get_bf16<kC, (VEC > 0)>(a.k, tt * a.ks + (int64_t)kh * DK + ch, nk[i]);
+        if constexpr (OUT) get_bf16<kC, (VEC > 0)>(a.q, tt * a.qs + (int64_t)kh * DK + ch, nq[i]);
         nb[i] = a.beta ? a.beta[tt * a.bs + h] : 1.0f;
       }
     }
     if (tid < kVP) {
-      const Tile<VEC> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, min(kB, sg.t1 - t), min(kDV, a.dv - v0));
+      const Tile<VEC == 2> tv(a.v, (int64_t)t * a.vs + head + v0, a.vs, min(kB, sg.t1 - t), min(kDV, a.dv - v0));
       nv = tv.load(tid / (kDV / 8), tid % (kDV / 8) * 8);
     }
   };
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
     if constexpr (OUT) {
       if (tid < kVP) {
         const int r = tid / (kDV / 8), c = tid % (kDV / 8) * 8;
-        const Tile<VEC> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
+        const Tile<VEC == 2> to(a.out, (int64_t)t * a.os + head + v0, a.os, n, min(kDV, a.dv - v0));
         to.store_step(r, c, 0, 0, *(const U4*)&so[r * kVR + c]);
       }
     }
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC ? 2 : 1) void k_scan_key(cons
     for (int j = 0; j < kC; ++j) g.total[((int64_t)s * a.H + h) * DK + ch + j] = whole[j];
 }
 
-template <int DK, int NV, bool VEC>
+template <int DK, int NV, int VEC>
 hipError_t key(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int vchunks = (a.dv + 64 * NV - 1) / (64 * NV);
   const uint32_t grid = (uint32_t)(g.count * a.H * vchunks);
@@ -355,8 +355,8 @@ hipError_t key_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   // 128 columns a workgroup halve the operands' preparation; 256 channels leave
   // no registers for them
   if constexpr (DK < 256)
-    if (a.dv > 64) return a.vec ? key<DK, 2, true>(a, g, s) : key<DK, 2, false>(a, g, s);
-  return a.vec ? key<DK, 1, true>(a, g, s) : key<DK, 1, false>(a, g, s);
+    if (a.dv > 64) return a.vec == 2 ? key<DK, 2, 2>(a, g, s) : a.vec ? key<DK, 2, 1>(a, g, s) : key<DK, 2, 0>(a, g, s);
+  return a.vec == 2 ? key<DK, 1, 2>(a, g, s) : a.vec ? key<DK, 1, 1>(a, g, s) : key<DK, 1, 0>(a, g, s);
 }
 
 }  // namespace
