@@ -8,9 +8,9 @@
 // and the state after the chunk is the last S_i.
 //
 // Precision: q, k and v are bf16, so a product with one of them is exact when
-// the other operand is cut into bf16 pieces: three pieces (24 bits) of w v in
-// the state's update, two (16 bits) of S and of P in the outputs, which are
-// rounded to bf16 at the end.  All sums are fp32.  c is summed in fp64:
+// the other operand, w v in the state's update, S and P in the outputs, is cut
+// into three bf16 pieces, which hold its 24 bits.  All sums are fp32; an output
+// is rounded to bf16 once.  c is summed in fp64:
 // differences of long sums of logs would lose the decays between neighbours;
 // a decay of zero counts as 2^-10000.
 //
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
   __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR];
   __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? kL * kKR : 8];
   __shared__ __attribute__((aligned(16))) uint16_t sv[kL * kVR];           // v, then the outputs
-  __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 2 : 1][OUT ? kL * kPR : 8];   // P's two pieces
+  __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 3 : 1][OUT ? kL * kPR : 8];   // P's three pieces
   __shared__ __attribute__((aligned(16))) float sc[2][kL];                 // c_i as a sum of two floats
   __shared__ __attribute__((aligned(16))) float se[kL], sw[kL], sb[kL];    // 2^{c_i}, weight in the update, beta
   __shared__ int sodd;
@@ -206,7 +206,6 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
             const int j = 16 * (jp + y) + 4 * q4;
             const F4 bj = *(const F4*)&sb[j];
             const F4 cj = *(const F4*)&sc[0][j], dj = *(const F4*)&sc[1][j];
-            uint32_t hi[2], lo[2];
             float f[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -214,13 +213,9 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
               const float w = p[y][r] * e * bj[r];
               f[r] = j + r <= i ? w : 0.0f;
             }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              hi[r] = upper2(f[2 * r], f[2 * r + 1]);
-              lo[r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
-            }
-            *(uint2*)&sp[0][i * kPR + j] = make_uint2(hi[0], hi[1]);
-            *(uint2*)&sp[1][i * kPR + j] = make_uint2(lo[0], lo[1]);
+            *(uint2*)&sp[0][i * kPR + j] = make_uint2(take2(f[0], f[1]), take2(f[2], f[3]));
+            *(uint2*)&sp[1][i * kPR + j] = make_uint2(take2(f[0], f[1]), take2(f[2], f[3]));
+            *(uint2*)&sp[2][i * kPR + j] = make_uint2(round2(f[0], f[1]), round2(f[2], f[3]));
           }
         }
       }
@@ -233,7 +228,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
         for (int i = 0; i < 4; ++i) O[v][i] = (F4){0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < kKS; ++c) {
-        BF8 sp_[NV][2];
+        BF8 sp_[NV][3];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           float f[8];
@@ -246,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
         for (int i = 0; i < 4; ++i) qf[i] = *(const BF8*)&sq[(16 * i + m) * kKR + 32 * c + 8 * q4];
         // products on one accumulator are kept apart: each takes several issue slots
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 3; ++x)
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -269,21 +264,19 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
           const uint16_t* x = &sv[(32 * c + 4 * q4 + (m >> 2)) * kVR + (wave * NV + v) * 16 + 4 * (m & 3)];
           ub[c][v] = join(read_tr(x), read_tr(x + 16 * kVR));
         }
-        BF8 ph[4], pl[4];
 #pragma unroll
-        for (int i = 2 * c; i < 4; ++i) {
-          const uint16_t* x = &sp[0][(16 * i + m) * kPR + 32 * c + 4 * q4];
-          const uint16_t* y = &sp[1][(16 * i + m) * kPR + 32 * c + 4 * q4];
-          ph[i] = join(*(const BF4*)x, *(const BF4*)(x + 16));
-          pl[i] = join(*(const BF4*)y, *(const BF4*)(y + 16));
-        }
+        for (int x = 0; x < 3; ++x) {
+          BF8 p[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int i = 2 * c; i < 4; ++i) {
+            const uint16_t* y = &sp[x][(16 * i + m) * kPR + 32 * c + 4 * q4];
+            p[i] = join(*(const BF4*)y, *(const BF4*)(y + 16));
+          }
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 2 * c; i < 4; ++i)
-              O[v][i] = mfma(x ? pl[i] : ph[i], ub[c][v], O[v][i]);
+            for (int i = 2 * c; i < 4; ++i) O[v][i] = mfma(p[i], ub[c][v], O[v][i]);
+        }
       }
       // ---- weighted v; then the outputs take v's place
       BF8 wu[NV][2][3];

@@ -27,8 +27,8 @@ __device__ __forceinline__ BF4 read_tr(const uint16_t* p) {
   return __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
 }
 
-// Eight floats as a sum of bf16 numbers, by cutting bits off: hi holds the
-// upper 8 significant bits, mid the next 8, lo the rest rounded.
+// Floats as a sum of bf16 numbers, each the rest rounded: three hold all 24 bits,
+// the second is at most 2^-9 of the number, the third 2^-18.
 __device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper halves of a and b
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
   using F2 = float __attribute__((ext_vector_type(2)));
   using B2 = __bf16 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(((F2){a, b}), B2));
+}
+// The next piece of two numbers, which are left with the rest.
+__device__ __forceinline__ uint32_t take2(float& a, float& b) {
+  const uint32_t d = round2(a, b);
+  a -= __uint_as_float(d << 16);
+  b -= __uint_as_float(d & 0xFFFF0000u);
+  return d;
 }
 template <int N>
 __device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
@@ -47,15 +54,7 @@ __device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
   for (int n = 0; n < N; ++n) {
     uint32_t d[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + 1 < N) {
-        d[j] = upper2(r[2 * j], r[2 * j + 1]);
-        r[2 * j] -= cut(r[2 * j]);
-        r[2 * j + 1] -= cut(r[2 * j + 1]);
-      } else {
-        d[j] = round2(r[2 * j], r[2 * j + 1]);
-      }
-    }
+    for (int j = 0; j < 4; ++j) d[j] = n + 1 < N ? take2(r[2 * j], r[2 * j + 1]) : round2(r[2 * j], r[2 * j + 1]);
     out[n] = __builtin_bit_cast(BF8, (U4){d[0], d[1], d[2], d[3]});
   }
 }
