@@ -14,12 +14,12 @@
 // chain bounds a long prompt: with T at hand a chunk is four products.
 //
 // Precision: q, k and v are bf16, so a product with one of them is exact when
-// the other operand is cut into bf16 pieces: three (24 bits) of S in S k and
-// of u in the update, two (16 bits) of S, P and u in the outputs, which are
-// rounded to bf16 at the end.  T is fp32, made and applied by fp32 matrix
-// instructions: its diagonal blocks of 16 by substitution, the others from
-// them; it is applied as three bf16 pieces by three of R, the six products that
-// reach 24 bits.  c is summed in fp64; a decay of zero counts as 2^-10000.
+// the other operand, S or u, is cut into three bf16 pieces, which hold its 24
+// bits.  T is fp32, made by fp32 matrix instructions: its diagonal blocks of 16
+// by substitution, the others from them.  T R and P u are products of three
+// pieces by three without the last three, at most 2^-27 of the whole each.
+// All sums are fp32, c's fp64; a decay of zero counts as 2^-10000; an output is
+// rounded to bf16 once.
 //
 // Where few heads leave compute units idle, long sequences go in pieces at once:
 // a pass for what each piece does to the state before it, a short chain over
@@ -42,7 +42,7 @@ namespace {
 constexpr int kGate = 256;                    // floats: 2^{c_i}, 2^{c_last - c_i}, beta_i, 2^{c_last}, oddness
 constexpr int kTile = 64 * 8 / 2;             // floats of a 16 x 32 tile in bf16, 8 elements a lane
 constexpr int kTri = 6 * 3 * kTile;           // T's lower tiles in three pieces
-constexpr int kPairs = 6 * 2 * kTile;         // P's lower tiles in two
+constexpr int kPairs = 6 * 2 * kTile;         // P's lower tiles in fp32
 constexpr int kPrepFloats = kGate + kTri + kPairs;
 static_assert(kPrepFloats * 4 == kScanPrepBytes, "workspace a chunk and head");
 
@@ -115,12 +115,11 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
           kk[y] = mfma(kj, ki, kk[y]);
         }
       }
-      U4 hi, lo;
+      F4* to = (F4*)(out + kGate + kTri) + piece(wave, jp >> 1) * 128 + lane;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int j = 16 * (jp + y) + 4 * q4;
-        float f[4];
-        F4 neg;
+        F4 f, neg;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float e = __builtin_amdgcn_exp2f((float)(ci - sc[j + r]));
@@ -128,16 +127,9 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
           f[r] = j + r <= i ? w : 0.0f;
           neg[r] = j + r < i ? z : 0.0f;
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          hi[2 * y + r] = upper2(f[2 * r], f[2 * r + 1]);
-          lo[2 * y + r] = round2(f[2 * r] - cut(f[2 * r]), f[2 * r + 1] - cut(f[2 * r + 1]));
-        }
         *(F4*)&sa[i * kAR + j] = neg;
+        to[64 * y] = f;                       // columns j .. j + 3
       }
-      U4* to = (U4*)(out + kGate + kTri) + piece(wave, jp >> 1) * 128 + lane;
-      to[0] = hi;
-      to[64] = lo;
     }
   }
   __syncthreads();
@@ -361,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           R[i] = mfma(kf[c & 1][i], sp[c & 1][y], R[i]);
-          if (OUT && y < 2) O[i] = mfma(qf[c & 1][i], sp[c & 1][y], O[i]);
+          if constexpr (OUT) O[i] = mfma(qf[c & 1][i], sp[c & 1][y], O[i]);
         }
       if (c + 1 < kKS) pieces(c + 1);
     }
@@ -391,12 +383,10 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       BF8 rp[3];
       split(f, rp);
       point(kKS + c);
-      // the six products of pieces that reach 24 bits
 #pragma unroll
       for (int p = 0; p < 6; ++p)
 #pragma unroll
-        for (int i = 2 * c; i < 4; ++i)
-          U[i] = mfma(T[i][p == 2 || p == 3 ? 1 : p == 5 ? 2 : 0], rp[p == 1 || p == 3 ? 1 : p == 4 ? 2 : 0], U[i]);
+        for (int i = 2 * c; i < 4; ++i) U[i] = mfma(T[i][first_of(p)], rp[second_of(p)], U[i]);
     }
     // ---- outputs: P u on top
     BF8 wu[2][3], kt[2][4];
@@ -411,12 +401,14 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     };
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      BF8 P[4][2];
+      BF8 P[4][3];
 #pragma unroll
-      for (int i = 2 * c; OUT && i < 4; ++i)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          P[i][y] = *(const BF8*)&b.prep[kGate + kTri + (2 * piece(i, c) + y) * kTile + lane * 4];
+      for (int i = 2 * c; OUT && i < 4; ++i) {
+        const float* from = &b.prep[kGate + kTri + 2 * piece(i, c) * kTile + lane * 4];
+        const F4 lo = *(const F4*)from, hi = *(const F4*)(from + 256);
+        const float p[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        split(p, P[i]);
+      }
       if (c == 1) columns(0);
       float f[8], g[8];
 #pragma unroll
@@ -428,13 +420,13 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
           g[4 * j + r] = U[2 * c + j][r] * w[r];
         }
       }
-      BF8 ub[2];
+      BF8 ub[3];
       split(f, ub);
       point(kKS + 2 + c);
 #pragma unroll
-      for (int y = 0; y < 3; ++y)
+      for (int y = 0; y < 6; ++y)
 #pragma unroll
-        for (int i = 2 * c; OUT && i < 4; ++i) O[i] = mfma(P[i][y == 1], ub[y == 2], O[i]);
+        for (int i = 2 * c; OUT && i < 4; ++i) O[i] = mfma(P[i][first_of(y)], ub[second_of(y)], O[i]);
       split(g, wu[c]);
     }
     // ---- the state

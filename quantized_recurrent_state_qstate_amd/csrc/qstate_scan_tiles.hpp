@@ -59,6 +59,11 @@ __device__ __forceinline__ void split(const float (&f)[8], BF8 (&out)[N]) {
   }
 }
 
+// Six products of three pieces by three; the other three are at most 2^-27 of
+// the whole each.  Product p takes pieces first_of(p) and second_of(p).
+__device__ constexpr int first_of(int p) { return p == 2 || p == 3 ? 1 : p == 5 ? 2 : 0; }
+__device__ constexpr int second_of(int p) { return p == 1 || p == 3 ? 1 : p == 4 ? 2 : 0; }
+
 __device__ __forceinline__ BF8 join(BF4 a, BF4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
