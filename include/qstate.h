@@ -346,9 +346,9 @@ qs_status qstate_qk_norm_rotate(const qstate_qk* a, void* stream);
  *   qstate_quantize takes), or `initial` for a sequence of no tokens.
  * decay must not be negative.  A decay of 0 forgets everything before its
  * token.  A value that is not finite reaches only its own token and later ones
- * of its sequence.  With bf16 inputs products take operands in bf16 pieces, two
- * for out (which is bf16) and three for the state; sums are fp32.  Strides of q,
- * k, v and out of up to 2^24 elements. */
+ * of its sequence.  With bf16 inputs products take the other operand in three
+ * bf16 pieces, which hold its 24 bits; sums are fp32, and an output is rounded to
+ * bf16 once.  Strides of q, k, v and out of up to 2^24 elements. */
 typedef struct {
   const void* q;
   const void* k;

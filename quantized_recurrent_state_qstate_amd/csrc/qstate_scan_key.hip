@@ -13,9 +13,10 @@
 // go token by token.  No logarithms: they would cost a rounding a token that
 // adds up over the state's memory.
 //
-// Precision: v is bf16; the other operands are cut into bf16 pieces: the state's
-// keys into three (24 bits), q D, k / D and S into two (16 bits) for the outputs,
-// which are rounded to bf16 at the end.  All sums are fp32.
+// Precision: v is bf16; the other operands (the state's keys, q D, k / D, S and
+// P) are cut into three bf16 pieces, which hold their 24 bits; products of three
+// by three leave out the last three, at most 2^-27 of the whole each.  All sums
+// are fp32; an output is rounded to bf16 once.
 //
 // A workgroup holds 64 NV value columns of one (segment, head), each wave 16 NV
 // in accumulators [dk][v].  Each wave prepares 4 of the block's 16 tokens.
@@ -57,27 +58,28 @@ __device__ __forceinline__ void get_bf16(const void* p, int64_t i, float (&f)[N]
   }
 }
 
-// The p-th bf16 piece of N numbers, which are left with the rest.
+// N numbers as three bf16 pieces, `next` elements apart.
 template <int N>
-__device__ __forceinline__ void put_piece(uint16_t* to, float (&f)[N], bool last) {
-  if constexpr (N == 1) {
-    const __bf16 b = (__bf16)f[0];
-    *to = last ? __builtin_bit_cast(uint16_t, b) : (uint16_t)(__float_as_uint(f[0]) >> 16);
-  } else {
+__device__ __forceinline__ void put_pieces(uint16_t* to, int next, float (&f)[N]) {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) *(uint32_t*)(to + j) = last ? round2(f[j], f[j + 1]) : upper2(f[j], f[j + 1]);
+  for (int p = 0; p < 3; ++p) {
+    if constexpr (N == 1) {
+      const __bf16 b = (__bf16)f[0];
+      to[p * next] = __builtin_bit_cast(uint16_t, b);
+      f[0] -= (float)b;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; j += 2) *(uint32_t*)(to + p * next + j) = take2(f[j], f[j + 1]);
+    }
   }
-  if (!last)
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[j] -= cut(f[j]);
 }
 
 template <int DK, int NV, bool OUT, int VEC>
 __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(const ScanArgs a, const ScanSegs g, int vchunks) {
   constexpr int kDV = 64 * NV, kKS = DK / 32, kC = DK / 64, kR = DK + 8, kVR = kDV + 8;
   constexpr int kVP = kB * kDV / 8;                                    // 16-byte pieces of v
-  __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? 2 : 1][OUT ? kB * kR : 8];   // q D
-  __shared__ __attribute__((aligned(16))) uint16_t sk[OUT ? 2 : 1][OUT ? kB * kR : 8];   // beta k / D
+  __shared__ __attribute__((aligned(16))) uint16_t sq[OUT ? 3 : 1][OUT ? kB * kR : 8];   // q D
+  __shared__ __attribute__((aligned(16))) uint16_t sk[OUT ? 3 : 1][OUT ? kB * kR : 8];   // beta k / D
   __shared__ __attribute__((aligned(16))) uint16_t su[3][kB * kR];                       // the state's keys
   __shared__ __attribute__((aligned(16))) uint16_t sv[kB * kVR];
   __shared__ __attribute__((aligned(16))) uint16_t so[OUT ? kB * kVR : 8];
@@ -190,19 +192,16 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
         high = max(high, __float_as_uint(kb) & 0x7FFFFFFFu);
         if constexpr (OUT) {
           x[j] = nq[i][j] * D;
-          y[j] = kb * __builtin_amdgcn_rcpf(D);   // for P alone, of 16 bits
+          const float inv = __builtin_amdgcn_rcpf(D);     // within 1 ulp; one Newton step
+          y[j] = kb * fmaf(fmaf(-D, inv, 1.0f), inv, inv);
         }
         z[j] = kb * (suf[i][j] * behind[j]);
       }
       if constexpr (OUT) {
-        put_piece<kC>(&sq[0][r * kR + ch], x, false);
-        put_piece<kC>(&sq[1][r * kR + ch], x, true);
-        put_piece<kC>(&sk[0][r * kR + ch], y, false);
-        put_piece<kC>(&sk[1][r * kR + ch], y, true);
+        put_pieces<kC>(&sq[0][r * kR + ch], kB * kR, x);
+        put_pieces<kC>(&sk[0][r * kR + ch], kB * kR, y);
       }
-      put_piece<kC>(&su[0][r * kR + ch], z, false);
-      put_piece<kC>(&su[1][r * kR + ch], z, false);
-      put_piece<kC>(&su[2][r * kR + ch], z, true);
+      put_pieces<kC>(&su[0][r * kR + ch], kB * kR, z);
     }
     if (OUT && (bad || far > 0x60000000u || high >= 0x7F800000u)) sodd[turn] = 1;
     if (tid == 0) sodd[turn ^ 1] = 0;        // read in the block before, next written in the next
@@ -247,43 +246,47 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
       if constexpr (OUT) {
         // ---- P (transposed: a lane gets 4 j of one i, which is the next product's operand)
         F4 p = (F4){0, 0, 0, 0}, O[NV];
-        BF8 qf[kKS][2];
+        BF8 qf[kKS][3];
 #pragma unroll
         for (int c = 0; c < kKS; ++c)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) qf[c][x] = *(const BF8*)&sq[x][m * kR + 32 * c + 8 * q4];
+          for (int x = 0; x < 3; ++x) qf[c][x] = *(const BF8*)&sq[x][m * kR + 32 * c + 8 * q4];
 #pragma unroll
         for (int c = 0; c < kKS; ++c) {
-          const BF8 kh0 = *(const BF8*)&sk[0][m * kR + 32 * c + 8 * q4], kh1 = *(const BF8*)&sk[1][m * kR + 32 * c + 8 * q4];
-          p = mfma(kh0, qf[c][0], p);
-          p = mfma(kh1, qf[c][0], p);
-          p = mfma(kh0, qf[c][1], p);
+          BF8 kd[3];
+#pragma unroll
+          for (int x = 0; x < 3; ++x) kd[x] = *(const BF8*)&sk[x][m * kR + 32 * c + 8 * q4];
+#pragma unroll
+          for (int x = 0; x < 6; ++x) p = mfma(kd[first_of(x)], qf[c][second_of(x)], p);
         }
         // ---- products with the state
 #pragma unroll
         for (int v = 0; v < NV; ++v) O[v] = (F4){0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < kKS; ++c)
+        for (int c = 0; c < kKS; ++c) {
+          BF8 sp[NV][3];
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            BF8 sp[2];
             float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = S[v][2 * c + (j >> 2)][j & 3];
-            split(f, sp);
-            O[v] = mfma(qf[c][0], sp[0], O[v]);
-            O[v] = mfma(qf[c][0], sp[1], O[v]);
-            O[v] = mfma(qf[c][1], sp[0], O[v]);
+            split(f, sp[v]);
           }
+#pragma unroll
+          for (int x = 0; x < 6; ++x)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) O[v] = mfma(qf[c][first_of(x)], sp[v][second_of(x)], O[v]);
+        }
         float f[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) f[r] = 4 * q4 + r <= m ? p[r] : 0.0f;
-        const uint2 hi = make_uint2(upper2(f[0], f[1]), upper2(f[2], f[3]));
-        const uint2 lo = make_uint2(round2(f[0] - cut(f[0]), f[1] - cut(f[1])), round2(f[2] - cut(f[2]), f[3] - cut(f[3])));
+        uint2 pp[3];
+#pragma unroll
+        for (int x = 0; x < 3; ++x) pp[x] = make_uint2(take2(f[0], f[1]), take2(f[2], f[3]));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          O[v] = mfma16(__builtin_bit_cast(BF4, hi), vf[v], O[v]);
-          O[v] = mfma16(__builtin_bit_cast(BF4, lo), vf[v], O[v]);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) O[v] = mfma16(__builtin_bit_cast(BF4, pp[x]), vf[v], O[v]);
           if (a.skip)
 #pragma unroll
             for (int r = 0; r < 4; ++r) O[v][r] = fmaf(skip, (float)vf[v][r], O[v][r]);

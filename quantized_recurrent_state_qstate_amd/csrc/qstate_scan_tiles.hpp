@@ -29,10 +29,6 @@ __device__ __forceinline__ BF4 read_tr(const uint16_t* p) {
 
 // Floats as a sum of bf16 numbers, each the rest rounded: three hold all 24 bits,
 // the second is at most 2^-9 of the number, the third 2^-18.
-__device__ __forceinline__ uint32_t upper2(float a, float b) {   // the upper halves of a and b
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t round2(float a, float b) {
   using F2 = float __attribute__((ext_vector_type(2)));
   using B2 = __bf16 __attribute__((ext_vector_type(2)));

@@ -27,7 +27,7 @@ from quantized_recurrent_state_qstate_amd import QState, StateConfig
 DEV = "cuda"
 U = 2.0 ** -24
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
-KINDS = [("additive", "head"), ("delta", "head"), ("delta", "key")]
+KINDS = [("additive", "head"), ("additive", "key"), ("delta", "head"), ("delta", "key")]
 
 
 def inputs(kind, decay, T, H, G, dk, dv, dtype, seed, mu):
