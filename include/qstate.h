@@ -384,7 +384,7 @@ typedef struct {
 
 /* Copy whole state slots: for i < n, slot dst_slot[i] of `pool` (the handle's
  * B slots) becomes slot src_slot[i] of `source` (src_slots slots of the same
- * configuration; may be the pool itself), or all zeros (the state S = 0) when
+ * configuration; may be the pool itself, src_slots <= B), or all zeros (the state S = 0) when
  * src_slot[i] is -1.  Forks (one source, many destinations), moves, clears,
  * and hands states from one pool to another in one launch.  Elements with a
  * slot out of range are skipped.  Destinations must be distinct, and within

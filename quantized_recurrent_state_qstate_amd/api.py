@@ -445,7 +445,7 @@ class QState:
                 raise ValueError("extra buffers of another pool need source_extra")
             m = int(source_slots)
         d = self._checked(pool, self.cfg.B)
-        s = d if source is pool else self._checked(source, m)
+        s = d if source is pool and m == self.cfg.B else self._checked(source, m)
         bufs, ne = self._extra(extra, source_extra, m) if extra or source_extra else (None, 0)
         _lib.check(_lib.lib().qstate_copy_slots(self._h, ctypes.byref(d), ctypes.byref(s), m, n, _ptr(src_slot),
                                                 _ptr(dst_slot), bufs, ne, raw_stream(stream, self.device)),

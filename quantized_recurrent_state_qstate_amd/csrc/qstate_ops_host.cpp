@@ -432,6 +432,8 @@ qs_status qstate_copy_slots(qstate_handle* h, const qstate_tensors* pool, const 
     if ((b.src == b.dst) != (a.buf[0].src == a.buf[0].dst))
       return op_fail(QS_EINVAL, "some of the source's buffers are the pool's and some are not");
   }
+  if (a.buf[0].src == a.buf[0].dst && src_slots > B)
+    return op_fail(QS_EINVAL, "%d slots of a source that is the pool, which has %d", src_slots, (int)B);
   if ((uint64_t)n * a.pieces > 0x7FFFFFFFull) return op_fail(QS_EUNSUPPORTED, "%d copies in one call", n);
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
   a.src_slots = src_slots;

@@ -232,6 +232,15 @@ int main() {
         CHECK(qstate_copy_slots(h, &p, &p, -1, 1, src, dst, nullptr, 0, nullptr) == QS_EINVAL);
         CHECK(qstate_copy_slots(h, &p, &p, 4, 1, nullptr, dst, nullptr, 0, nullptr) == QS_EINVAL);
         CHECK(qstate_copy_slots(h, &p, nullptr, 4, 1, src, dst, nullptr, 0, nullptr) == QS_EINVAL);
+        // the pool as its own source has no more slots than the pool
+        {
+          const int before = g_launches;
+          CHECK(qstate_copy_slots(h, &p, &p, 5, 1, src, dst, nullptr, 0, nullptr) == QS_EINVAL);
+          qstate_tensors again = p;
+          CHECK(qstate_copy_slots(h, &p, &again, 1 << 20, 1, src, dst, nullptr, 0, nullptr) == QS_EINVAL);
+          CHECK(g_launches == before);
+          CHECK(qstate_copy_slots(h, &p, &p, 3, 1, src, dst, nullptr, 0, nullptr) == QS_OK && g_slots.src_slots == 3);
+        }
         qstate_tensors shifted = p, mixed = o;
         shifted.codes = at((1ull << 32) + 16);
         CHECK(qstate_copy_slots(h, &p, &shifted, 4, 1, src, dst, nullptr, 0, nullptr) == QS_EINVAL);

@@ -5,8 +5,8 @@ import ctypes
 import pytest
 import torch
 
-from quantized_recurrent_state_qstate_amd import _lib, causal_conv, causal_conv_step, qk_norm_rotate
-from quantized_recurrent_state_qstate_amd.api import check_rows
+from quantized_recurrent_state_qstate_amd import QState, StateConfig, _lib, causal_conv, causal_conv_step, plan, qk_norm_rotate
+from quantized_recurrent_state_qstate_amd.api import _ITEM, _state_dtypes, check_rows
 
 A = 1 << 20        # an address that is never read: every call here is refused first
 
@@ -161,3 +161,22 @@ def test_handle_calls_host_code_under_sanitizers(tmp_path):
                 "-I", csrc, os.path.join(csrc, "qstate_host.cpp"), os.path.join(csrc, "qstate_ops_host.cpp"),
                 os.path.join(HERE, "ops_driver.cpp"), "-o", exe], exe)
     assert "0 failed checks" in out, out
+
+
+def handle(**kw):
+    """A QState without a device: its checks of arguments, on CPU tensors, end before the library is called."""
+    qs = QState.__new__(QState)
+    qs.cfg, qs.device, qs._h = StateConfig(**kw), torch.device("cpu"), ctypes.c_void_p()
+    qs.sizes, qs._scan_bytes = plan(qs.cfg), {}
+    qs._buffers = [(n, f"state[{n!r}]", getattr(torch, dt), qs.sizes[n] // _ITEM[dt])
+                   for n, dt in _state_dtypes(qs.cfg).items() if qs.sizes[n]]
+    return qs
+
+
+@pytest.mark.parametrize("m", [3, 1 << 20])
+def test_the_pool_as_its_own_source_has_no_more_slots(m):
+    qs = handle(B=2, H=2, dk=64, dv=16)
+    pool = qs.new_state()
+    idx = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="state\\['codes'\\]: .* expected at least"):
+        qs.copy_slots(pool, idx, idx, source=pool, source_slots=m)
