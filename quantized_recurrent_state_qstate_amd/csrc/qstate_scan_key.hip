@@ -8,10 +8,10 @@
 // and the state after the block is the last S_i, whose keys beta_j k_j D_last / D_j
 // are formed with the products of the decays behind j, not by division.
 //
-// A block is 16 tokens because 1 / D_j has to stay in range: blocks in which
-// D leaves [2^-96, 2^96] (decays below 1/64 all along) or a value is not finite
-// go token by token.  No logarithms: they would cost a rounding a token that
-// adds up over the state's memory.
+// A block is 16 tokens because 1 / D_j has to stay in range: blocks in which D
+// leaves [2^-100, 2^20] (decays below 1/64 all along), beta k / D or q D leaves what
+// three bf16 pieces hold, or a value is not finite go token by token.  No
+// logarithms: they would cost a rounding a token that adds up over the state's memory.
 //
 // Precision: v is bf16; the other operands (the state's keys, q D, k / D, S and
 // P) are cut into three bf16 pieces, which hold their 24 bits; products of three
@@ -165,7 +165,8 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
     if (tid < kVP) *(U4*)&sv[tid / (kDV / 8) * kVR + tid % (kDV / 8) * 8] = nv;
     __syncthreads();                         // products are there; the block before has been read
     // ---- the operands
-    uint32_t far = 0, high = 0;
+    uint32_t far = 0, low = 0xFFFFFFFFu;
+    int32_t high = 0;
     float before[kC], behind[kC];
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
@@ -187,10 +188,14 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         const float D = before[j] * pre[i][j], kb = nk[i][j] * nb[i];
-        // D in [2^-96, 2^96] and kb finite, on the bits: the largest of each over the tokens
-        far = max(far, __float_as_uint(D) - 0x0F800000u);
-        high = max(high, __float_as_uint(kb) & 0x7FFFFFFFu);
         if constexpr (OUT) {
+          // On the bits, whose sums and differences are products and quotients to a factor
+          // of 2: D in [2^-100, 2^20]; |kb| / D up to 2^100, which a kb that is not finite exceeds;
+          // |q| D from 2^-100 on where q is not zero, so that its third piece is a normal number.
+          const uint32_t bits = __float_as_uint(D);
+          far = max(far, bits - (27u << 23));
+          high = max(high, (int32_t)((__float_as_uint(kb) & 0x7FFFFFFFu) - bits));
+          low = min(low, __builtin_elementwise_add_sat((__float_as_uint(nq[i][j]) & 0x7FFFFFFFu) - 1u, bits));
           x[j] = nq[i][j] * D;
           const float inv = __builtin_amdgcn_rcpf(D);     // within 1 ulp; one Newton step
           y[j] = kb * fmaf(fmaf(-D, inv, 1.0f), inv, inv);
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
       }
       put_pieces<kC>(&su[0][r * kR + ch], kB * kR, z);
     }
-    if (OUT && (bad || far > 0x60000000u || high >= 0x7F800000u)) sodd[turn] = 1;
+    if (OUT && (bad || far > 120u << 23 || high > 100 << 23 || low < 154u << 23)) sodd[turn] = 1;
     if (tid == 0) sodd[turn ^ 1] = 0;        // read in the block before, next written in the next
     __syncthreads();
     if (t + kB < sg.t1) fetch(t + kB);
