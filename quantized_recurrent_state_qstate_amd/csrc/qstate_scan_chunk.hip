@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
   __shared__ __attribute__((aligned(16))) uint16_t sp[OUT ? 3 : 1][OUT ? kL * kPR : 8];   // P's three pieces
   __shared__ __attribute__((aligned(16))) float sc[2][kL];                 // c_i as a sum of two floats
   __shared__ __attribute__((aligned(16))) float se[kL], sw[kL], sb[kL];    // 2^{c_i}, weight in the update, beta
-  __shared__ int sodd;
+  __shared__ int sgrow;
 
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, q4 = lane >> 4;
@@ -131,21 +131,13 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
     }
   };
 
-  if (tid == 0) sodd = 0;
   double total = 0.0;
+  [[maybe_unused]] bool lost[NV] = {};       // this lane's columns whose state is not finite any more
   fetch(sg.t0, sg.t1);
-  __syncthreads();
   for (int t = sg.t0; t < sg.t1;) {
     const int n = min(kL, sg.t1 - t);
     // ---- this chunk into LDS; gates
-    if constexpr (OUT) {
-      H2 most = (H2){0, 0};
-#pragma unroll
-      for (int i = 0; i < kVP; ++i) most = largest(most, nv[i]);
-      if (odd(most)) sodd = 1;
-    }
-    __syncthreads();                         // the chunk before has been read; sodd is known
-    const bool whole = !OUT || sodd == 0;
+    __syncthreads();                         // the chunk before has been read
 #pragma unroll
     for (int i = 0; i < kKP; ++i) {
       *(U4*)&sk[kr * kKR + kc + i * (kKStep * kKR)] = nk[i];
@@ -159,29 +151,18 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
       sc[0][lane] = (float)c;
       sc[1][lane] = (float)(c - (double)(float)c);
       sb[lane] = nb;
-      se[lane] = __builtin_amdgcn_exp2f((float)c);
-      sw[lane] = __builtin_amdgcn_exp2f((float)(all - c)) * nb;
+      const float e = __builtin_amdgcn_exp2f((float)c), w = __builtin_amdgcn_exp2f((float)(all - c));
+      se[lane] = e;
+      sw[lane] = w * nb;
+      if constexpr (OUT) sgrow = __ballot(e >= 0x1p100f || w >= 0x1p100f) != 0;
     }
     __syncthreads();
-    if (OUT && tid == 0) sodd = 0;           // read by all, and next written behind the chunk's last barrier
     const int next = t + n;
     if (next < sg.t1) fetch(next, sg.t1);
     if constexpr (!OUT) total += (double)sc[0][kL - 1] + (double)sc[1][kL - 1];
     const float eall = se[kL - 1];
 
-    if (OUT && !whole) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        by_token<DK, false>(
-            a, t, n, h, [&](int i, int c) { return *(const BF8*)&sk[i * kKR + c]; },
-            [&](int i, int c) { return *(const BF8*)&sq[i * kKR + c]; },
-            [&](int i) { return __uint_as_float((uint32_t)sv[i * kVR + (wave * NV + v) * 16 + m] << 16); },
-            [&](int i, float o) {
-              const __bf16 y = (__bf16)o;
-              sv[i * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
-            },
-            S[v]);
-    } else if constexpr (OUT) {
+    if constexpr (OUT) {
       // ---- P (transposed tiles: a lane gets 4 j of one i)
 #pragma unroll
       for (int x = 0; x < 4 / WAVES; ++x) {
@@ -303,16 +284,61 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
             for (int j = 0; j < 8; ++j)
               O[v][2 * c + (j >> 2)][j & 3] = fmaf(skip, (float)ub[c][v][j], O[v][2 * c + (j >> 2)][j & 3]);
       }
+      // ---- An output that is not finite, or nearly so: a value that was not, which the
+      // zeros in P bring to earlier tokens, or products that leave fp32 where the
+      // recurrence does not.  Then the outputs are made token by token; the state too, if
+      // it is v or decays that grow, else (a query) it is taken back from its place in memory.
+      bool out_of_range = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int v = 0; v < NV; ++v) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int i = 0; i < 4; ++i) top = highest(top, O[v][i]);
+        out_of_range |= top >= kHuge && !lost[v];
+      }
+      if (sgrow || __ballot(out_of_range)) {
+        H2 most = (H2){0, 0};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const __bf16 y = (__bf16)O[v][i][r];
-            sv[(16 * i + 4 * q4 + r) * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
-          }
-      update(wu, eall);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int v = 0; v < NV; ++v) most = largest(most, __builtin_bit_cast(U4, ub[c][v]));
+        const bool anew = sgrow || __ballot(odd(most));
+        float* kept = sg.last ? a.final + (int64_t)sg.seq * a.H * a.dv * DK : g.states + (int64_t)s * a.H * a.dv * DK;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int col = v0 + vcol + 16 * v;
+          if (!anew && col < a.dv)
+#pragma unroll
+            for (int y = 0; y < 2 * kKS; ++y)
+              *(F4*)(kept + (head + col) * DK + 32 * (y >> 1) + 8 * q4 + 4 * (y & 1)) = S[v][y];
+          by_token<DK, false>(
+              a, t, n, h, [&](int i, int c) { return *(const BF8*)&sk[i * kKR + c]; },
+              [&](int i, int c) { return *(const BF8*)&sq[i * kKR + c]; },
+              [&](int i) { return __uint_as_float((uint32_t)sv[i * kVR + (wave * NV + v) * 16 + m] << 16); },
+              [&](int i, float o) {
+                const __bf16 y = (__bf16)o;
+                sv[i * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+              },
+              S[v]);
+          lost[v] = spoiled(S[v]);
+          if (!anew && col < a.dv)
+#pragma unroll
+            for (int y = 0; y < 2 * kKS; ++y)
+              S[v][y] = *(const F4*)(kept + (head + col) * DK + 32 * (y >> 1) + 8 * q4 + 4 * (y & 1));
+        }
+        if (!anew) update(wu, eall);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const __bf16 y = (__bf16)O[v][i][r];
+              sv[(16 * i + 4 * q4 + r) * kVR + (wave * NV + v) * 16 + m] = __builtin_bit_cast(uint16_t, y);
+            }
+        update(wu, eall);
+      }
     } else {
       BF8 wu[NV][2][3];
 #pragma unroll

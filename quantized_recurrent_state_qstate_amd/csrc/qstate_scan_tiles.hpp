@@ -224,6 +224,28 @@ __device__ __forceinline__ H2 largest(H2 x, U4 u) {
 }
 __device__ __forceinline__ bool odd(H2 x) { return x[0] >= 0x7F80 || x[1] >= 0x7F80; }   // infinity or NaN
 
+// The largest magnitude of fp32 numbers, as bits; NaN is the largest.  From kHuge
+// (2^120) on a chunk's numbers count as out of fp32's range.
+constexpr uint32_t kHuge = (120u + 127u) << 23;
+__device__ __forceinline__ uint32_t highest(uint32_t top, F4 x) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(x[r]) & 0x7FFFFFFFu);
+  return top;
+}
+
+// Whether the lane's column of a state (in the scans' tiles, below) has a value that
+// is not finite: then all its later outputs are not, in whichever way they are made.
+template <int N>
+__device__ __forceinline__ bool spoiled(const F4 (&S)[N]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int y = 0; y < N; ++y) top = highest(top, S[y]);
+  uint64_t b = __ballot(top >= 0x7F800000u);
+  b |= b >> 32;
+  b |= b >> 16;
+  return (b >> (threadIdx.x & 15u) & 1u) != 0;
+}
+
 // Element (r, c) of an LDS tile with rows of N elements.  The 16-byte pieces of
 // a row are exchanged by the row's low bits, so that both ways of reading, 8
 // channels of 16 rows and (transposed) 4 rows of 4 x 4 channels, meet every
@@ -237,9 +259,9 @@ __device__ __forceinline__ int at(int r, int c) {
   return r * N + (((c >> 3) ^ flip<N>(r)) << 3) + (c & 7);
 }
 
-// A chunk token by token, for one with a value that is not finite: in the
-// products of a whole chunk a zero times such a value would reach the tokens
-// before it.  The state tiles are those of the scans (lane m, q4: column m,
+// A chunk token by token, for one with a value that is not finite, or that is
+// not in the products of a whole chunk: there a zero times such a value would
+// reach the tokens before it.  The state tiles are those of the scans (lane m, q4: column m,
 // channels 32 i + 8 q4 .. + 7); K(i, c) and Q(i, c) give 8 channels from c on
 // of token i, V(i) the lane's v, and O(i, o) takes the output.
 template <int DK, bool DELTA, class FK, class FQ, class FV, class FO>

@@ -77,3 +77,36 @@ def test_scan_small_query_behind_small_decays():
     a["decay"][32:] = 1.0
     a["q"][16:32] *= 2.0 ** -44
     right("additive", "bf16", a, *scan("additive", "key", "bf16", a))
+
+
+def test_scan_overflowing_sum_before_its_decay():
+    """Additive, a decay a head: S q leaves fp32, 2^c S q does not."""
+    a = make("additive", "head", 128, 2, 2, 64, 32, "bf16")
+    S0 = torch.randn(1, 2, 32, 64) * 2.0 ** 70
+    a["q"][40] *= 2.0 ** 60
+    a["decay"][:40] = 0.125
+    right("additive", "bf16", a, *scan("additive", "head", "bf16", a, initial=S0), initial=S0)
+
+
+GROWING = [("additive", "head", "bf16")]
+
+
+@pytest.mark.parametrize("kind,decay,dtype", GROWING)
+def test_scan_growing_decays_of_nothing(kind, decay, dtype):
+    """Decays above one whose product leaves fp32, while the state is still zero."""
+    a = make(kind, decay, 130, 2, 1, 64, 48, dtype)
+    for t in (0, 64):
+        a["decay"][t:t + 6] = 1e30
+    a["v"][:70] = 0
+    right(kind, dtype, a, *scan(kind, decay, dtype, a))
+
+
+@pytest.mark.parametrize("kind,decay,dtype", GROWING)
+def test_scan_growing_decays_of_little(kind, decay, dtype):
+    """... or so small that the product with it is not large."""
+    a = make(kind, decay, 130, 2, 1, 64, 48, dtype)
+    a["decay"][20:24] = 2.0 ** 33
+    a["v"][:24] *= 2.0 ** -100
+    a["v"][24:30] = 0
+    a["decay"][24:30] = 2.0 ** -6
+    right(kind, dtype, a, *scan(kind, decay, dtype, a))
