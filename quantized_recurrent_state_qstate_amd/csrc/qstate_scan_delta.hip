@@ -90,14 +90,15 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
     const double all = __shfl(c, 63);
     sc[lane] = c;
     sb[lane] = b;
-    out[lane] = __builtin_amdgcn_exp2f((float)c);
-    out[64 + lane] = __builtin_amdgcn_exp2f((float)(all - c));
+    const float e = __builtin_amdgcn_exp2f((float)c), w = __builtin_amdgcn_exp2f((float)(all - c));
+    out[lane] = e;
+    out[64 + lane] = w;
     out[128 + lane] = b;
-    if (!(fabsf(d) < INFINITY && fabsf(b) < INFINITY)) sodd = 1.0f;
+    if (!(fabsf(d) < INFINITY && fabsf(b) < INFINITY && e < 0x1p100f && w < 0x1p100f)) sodd = 1.0f;
     if (lane == 0) out[192] = __builtin_amdgcn_exp2f((float)all);
   }
   __syncthreads();
-  if (tid == 0) out[193] = sodd;            // k or a gate is not finite
+  if (tid == 0) out[193] = sodd;            // k or a gate is not finite, or the decays grow out of fp32
   // ---- P and A, transposed tiles: a lane gets 4 j of one i; wave i takes rows 16 i ..
   {
     const int i = 16 * wave + m;
@@ -270,6 +271,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
     };
   };
 
+  bool lost = false;                         // this lane's column has a state that is not finite any more
   int done_t = 0, done_n = 0;                // the chunk whose outputs wait in `so`
   auto put_out = [&]() {
 #pragma unroll
@@ -307,21 +309,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       const uint2 u = __builtin_bit_cast(uint2, x[i]);
       most = largest(most, (U4){u.x, u.y, 0, 0});
     }
-    if (b.prep[193] != 0.0f || __ballot(odd(most)) != 0) {
-      if constexpr (kTwo)
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) bring(i);
-      by_token<DK, true>(
-          a, t, n, h, [&](int i, int c) { return *(const BF8*)&b.k[at<DK>(i, c)]; },
-          [&](int i, int c) { return *(const BF8*)&(OUT ? b.q : b.k)[at<DK>(i, c)]; },
-          [&](int i) { return __uint_as_float((uint32_t)b.v[at<kDV>(i, col)] << 16); },
-          [&](int i, float o) {
-            const __bf16 y = (__bf16)o;
-            so[wave][i * 16 + m] = __builtin_bit_cast(uint16_t, y);
-          },
-          S);
-      return;
-    }
+    const bool odd_in = b.prep[193] != 0.0f || __ballot(odd(most)) != 0;
     // ---- products with the state
     F4 O[4], R[4];
 #pragma unroll
@@ -429,6 +417,41 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
         for (int i = 2 * c; OUT && i < 4; ++i) O[i] = mfma(P[i][first_of(y)], ub[second_of(y)], O[i]);
       split(g, wu[c]);
     }
+    // ---- A chunk with a value that is not finite, or nearly so, is made again token
+    // by token: a zero in T or P times it would reach earlier tokens, and products may
+    // leave fp32 where the recurrence does not.  If it is the outputs alone (a query),
+    // the state is taken back from its place in memory.
+    uint32_t top = 0, otop = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top = highest(top, U[i]);
+      if constexpr (OUT) otop = highest(otop, O[i]);
+    }
+    const bool anew = odd_in || __ballot(top >= kHuge && !lost), again = anew || __ballot(otop >= kHuge && !lost);
+    if (again) {
+      float* kept = OUT && piece_of.last ? a.final + at_state : carry + at_carry;
+      if (!anew && real)
+#pragma unroll
+        for (int y = 0; y < 2 * kKS; ++y) *(F4*)(kept + 32 * (y >> 1) + 4 * (y & 1)) = S[y];
+      by_token<DK, true>(
+          a, t, n, h, [&](int i, int c) { return *(const BF8*)&b.k[at<DK>(i, c)]; },
+          [&](int i, int c) { return *(const BF8*)&(OUT ? b.q : b.k)[at<DK>(i, c)]; },
+          [&](int i) { return __uint_as_float((uint32_t)b.v[at<kDV>(i, col)] << 16); },
+          [&](int i, float o) {
+            const __bf16 y = (__bf16)o;
+            so[wave][i * 16 + m] = __builtin_bit_cast(uint16_t, y);
+          },
+          S);
+      lost = spoiled(S);
+      if (anew) {
+        point(kKS + 4);
+        point(kKS + 5);
+        return;
+      }
+      if (real)
+#pragma unroll
+        for (int y = 0; y < 2 * kKS; ++y) S[y] = *(const F4*)(kept + 32 * (y >> 1) + 4 * (y & 1));
+    }
     // ---- the state
     const float eall = b.prep[192];
 #pragma unroll
@@ -445,7 +468,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
       for (int p = 0; p < 3; ++p)
 #pragma unroll
         for (int y = 0; y < 4; ++y) S[t4 + y] = mfma(kt[z & 1][y], wu[c][p], S[t4 + y]);
-      if (OUT && z < 2)                      // the outputs, behind the products that made them
+      if (OUT && z < 2 && !again)            // the outputs, behind the products that made them
 #pragma unroll
         for (int i = 2 * z; i < 2 * z + 2; ++i)
 #pragma unroll

@@ -79,6 +79,21 @@ def test_scan_small_query_behind_small_decays():
     right("additive", "bf16", a, *scan("additive", "key", "bf16", a))
 
 
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("T", [150, 2600])
+def test_scan_overflowing_product_does_not_reach_earlier_tokens(kind, decay, T):
+    """A finite key whose product with the state is not: outputs before it stay as they are."""
+    bad = T // 2 + 5
+    a = make(kind, decay, T, 2, 2, 64, 48, "bf16")
+    S0 = torch.randn(1, 2, 48, 64) * 8
+    clean, _ = scan(kind, decay, "bf16", a, initial=S0)
+    a["k"][bad, 0] = 3e38
+    a["q"][bad:] *= 1e-3
+    out, _ = scan(kind, decay, "bf16", a, initial=S0)
+    assert torch.isfinite(out[:bad]).all() and torch.allclose(out[:bad], clean[:bad], rtol=2 ** -7, atol=1e-3)
+    assert torch.isfinite(out[:, 1]).all()
+
+
 def test_scan_overflowing_sum_before_its_decay():
     """Additive, a decay a head: S q leaves fp32, 2^c S q does not."""
     a = make("additive", "head", 128, 2, 2, 64, 32, "bf16")
@@ -88,7 +103,7 @@ def test_scan_overflowing_sum_before_its_decay():
     right("additive", "bf16", a, *scan("additive", "head", "bf16", a, initial=S0), initial=S0)
 
 
-GROWING = [("additive", "head", "bf16")]
+GROWING = [("additive", "head", "bf16"), ("delta", "head", "bf16")]
 
 
 @pytest.mark.parametrize("kind,decay,dtype", GROWING)
