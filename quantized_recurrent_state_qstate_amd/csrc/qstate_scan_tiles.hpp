@@ -155,7 +155,8 @@ template <int N>
 __device__ __forceinline__ int flip(int r);
 
 // 64 rows of a bf16 tensor from row t0's element `p` on, `n` of them real: 16-byte
-// pieces of `width` elements, zeros behind the last row.  VEC: buffer loads,
+// pieces of `width` elements, zeros behind the last row and from column `width` on
+// (what lies there is another head's, or not of the tensor).  VEC: buffer loads,
 // whose bound is the last real row's end (rows are at most 2^24 elements
 // apart, so offsets fit; a piece that begins in a row begins in front of the
 // bound, and pieces are 16-byte aligned within it).
@@ -170,9 +171,13 @@ struct Tile {
     if constexpr (VEC)
       rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, n > 0 ? ((n - 1) * stride + width) * 2 : 0, 0x00027000);
   }
+  // Byte offset of (r, c); beyond every bound, whatever rows are added, from column `width` on.
+  __device__ __forceinline__ uint32_t offset(int r, int c) const {
+    return c < width ? (uint32_t)((r * stride + c) * 2) : 0x80000000u;
+  }
   __device__ __forceinline__ U4 load(int r, int c) const {
     if constexpr (VEC) {
-      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (r * stride + c) * 2, 0, 0));
+      return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(r, c), 0, 0));
     } else {
       uint32_t d[4];
 #pragma unroll
@@ -187,7 +192,7 @@ struct Tile {
   // Piece i of several that lie `step` rows apart from row r on: one product, then sums.
   __device__ __forceinline__ U4 load_step(int r, int c, int i, int step) const {
     if constexpr (VEC) {
-      const int at = (r * stride + c) * 2 + i * (step * stride * 2);
+      const uint32_t at = offset(r, c) + (uint32_t)(i * (step * stride * 2));
       return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
     } else {
       return load(r + i * step, c);
@@ -196,8 +201,7 @@ struct Tile {
   // The same way back; nothing at or behind the bound, or from column `width` on.
   __device__ __forceinline__ void store_step(int r, int c, int i, int step, U4 y) const {
     if constexpr (VEC) {
-      const uint32_t at = c < width ? (uint32_t)((r * stride + c) * 2) : 0x80000000u;
-      __builtin_amdgcn_raw_buffer_store_b128(y, rsrc, at + (uint32_t)(i * (step * stride * 2)), 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(y, rsrc, offset(r, c) + (uint32_t)(i * (step * stride * 2)), 0, 0);
     } else {
       uint16_t* o = (uint16_t*)p + (int64_t)(r + i * step) * stride + c;
       if (r + i * step < n)
@@ -210,7 +214,7 @@ struct Tile {
   template <int N>
   __device__ __forceinline__ void bring(uint16_t* tile, int e, int lane) const {
     const int r = (e + lane * 8) / N, c = (((lane * 8) % N / 8) ^ flip<N>(r)) * 8;
-    if constexpr (VEC) to_lds(rsrc, tile + e, (r * stride + c) * 2);
+    if constexpr (VEC) to_lds(rsrc, tile + e, (int)offset(r, c));
     else *(U4*)(tile + e + lane * 8) = load(r, c);
   }
 };

@@ -405,3 +405,27 @@ def test_scan_delta_in_pieces_odd_values(where, value, dtype, decay):
     else:
         assert not torch.isfinite(out[bad:, 0]).any() and not torch.isfinite(fin[0, 0]).any()
     qs.close()
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("dk,dv", [(64, 24), (128, 72), (128, 136)])
+def test_scan_what_lies_between_value_rows_does_not_matter(kind, decay, dk, dv):
+    """v as a slice of a wider tensor: the elements behind its last head, and another head's, change no bit."""
+    T, H = 300, 2
+    q, k, v, d, b = (x.to(DEV) for x in inputs(kind, decay, [T], H, 1, dk, dv, "bf16"))
+    qs = QState(StateConfig(kind=kind, decay_mode=decay, B=1, H=H, dk=dk, dv=dv))
+
+    def scan(behind, second):
+        wide = torch.full((T, H * dv + 64), behind, dtype=torch.bfloat16, device=DEV)
+        wide[:, :H * dv] = v.flatten(1)
+        if second is not None:
+            wide[:, dv:H * dv] = second
+        out = qs.scan(q, k, wide[:, :H * dv].unflatten(1, (H, dv)), d, b)
+        torch.cuda.synchronize()
+        return out
+
+    nan = float("nan")
+    (o, f), (o1, f1), (o2, f2) = scan(0.0, None), scan(nan, None), scan(0.0, nan)
+    assert torch.equal(o, o1) and torch.equal(f, f1)
+    assert torch.equal(o[:, 0], o2[:, 0]) and torch.equal(f[:, 0], f2[:, 0])
+    qs.close()
