@@ -102,6 +102,7 @@ struct ScanSegs {
   int32_t seg, count, cut;
   float* states;           // [count][H][dv][dk], null: no sequence is cut; delta rule: [count][H] kScanPrepBytes
   float* total;            // [count][H] or [count][H][dk]: a segment's whole decay; delta rule: L and M
+  int32_t* uncut;          // [n][H] where sequences are cut: not 0 if this one's outputs are made in one piece
 };
 constexpr int kScanPrepBytes = 1024 + 18 * 1024 + 12 * 1024;
 hipError_t launch_scan_key(const ScanArgs& a, const ScanSegs& g, hipStream_t s);

@@ -228,12 +228,13 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
 struct ScanPlan {
   bool chunked;
   qs::ScanSegs segs;
-  uint64_t states, total;   // workspace bytes
+  uint64_t states, total, uncut;   // workspace bytes
 };
 // Sequences of more than 2 cut tokens in pieces (delta rule).
 static void set_pieces(const qs::ScanArgs& a, int64_t cut, ScanPlan* p) {
   p->segs.cut = (int32_t)cut;
   p->total = (uint64_t)((a.T - 1) / cut + a.n) * (uint64_t)a.H * (uint64_t)(a.dv + a.dk) * (uint64_t)a.dk * 4u;
+  p->uncut = (uint64_t)a.n * (uint64_t)a.H * 4u;
 }
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
@@ -278,6 +279,7 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);
   p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)a.dv * (uint64_t)a.dk * 4u;
   p.total = ((uint64_t)p.segs.count * (uint64_t)a.H * (a.key ? (uint64_t)a.dk : 1u) * 4u + 255u) / 256u * 256u;
+  p.uncut = (uint64_t)a.n * (uint64_t)a.H * 4u;
   return p;
 }
 
@@ -287,7 +289,7 @@ qs_status qstate_scan_workspace(const qstate_handle* h, const qstate_scan_args* 
   qs_status s = check_scan(h, c, &a);
   if (s != QS_OK) return s;
   const ScanPlan p = scan_plan(a);
-  *bytes = p.states + p.total;
+  *bytes = p.states + p.total + p.uncut;
   return op_ok();
 }
 
@@ -321,17 +323,18 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   if (overlap(out, fin) || overlap(out, ini) || (c->initial != c->final && overlap(ini, fin)))
     return op_fail(QS_EINVAL, "an output overlaps another or the initial state");
   ScanPlan p = scan_plan(a);
-  if (p.states + p.total) {
-    if (!workspace || !aligned(workspace, 256) || bytes < p.states + p.total)
+  if (const uint64_t need = p.states + p.total + p.uncut) {
+    if (!workspace || !aligned(workspace, 256) || bytes < need)
       return op_fail(QS_EINVAL, "workspace of %llu bytes, %llu needed, 256-byte aligned", (unsigned long long)bytes,
-                     (unsigned long long)(p.states + p.total));
-    const Rows w{workspace, (int64_t)(p.states + p.total), (int64_t)(p.states + p.total), 1};
+                     (unsigned long long)need);
+    const Rows w{workspace, (int64_t)need, (int64_t)need, 1};
     for (const Rows& r : ins)
       if (overlap(r, w)) return op_fail(QS_EINVAL, "the workspace overlaps an input");
     if (overlap(w, fin) || overlap(w, ini) || overlap(w, out))
       return op_fail(QS_EINVAL, "the workspace overlaps an output or the initial state");
     p.segs.total = (float*)workspace;
     if (p.states) p.segs.states = (float*)((char*)workspace + p.total);
+    if (p.uncut) p.segs.uncut = (int32_t*)((char*)workspace + p.total + p.states);
   }
   if ((int64_t)p.segs.count * a.H * ((a.dv + 31) / 32) > 0x7FFFFFFF ||
       (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > 0x7FFFFFFF)

@@ -90,10 +90,12 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
     seg = find_piece(a, gs.cut, sid);
   } else {
     const Segment x = find_segment(a, gs.seg, sid);
-    seg = {x.seq, x.t0, x.t1, x.first, x.last, x.none};
+    seg = {x.seq, x.t0, x.t1, x.first, x.last, x.none, x.end};
   }
   const bool matrix = DELTA && !OUT && rc >= rchunks;   // rows of M
+  if (OUT && !seg.none) outputs_of(seg, a, gs, h);
   if (seg.none || (!OUT && (seg.last || (matrix && seg.first)))) return;
+  if (!OUT && seg.first && rc == 0 && threadIdx.x == 0) gs.uncut[(int64_t)seg.seq * a.H + h] = 0;
   const int t0 = seg.t0, t1 = seg.t1;
   const int sub = tid & 15, row = (tid >> 4) * RPL;   // this lane's channels and first row
   const int r0 = (matrix ? rc - rchunks : rc) * kRows, rows = matrix ? DK : a.dv;

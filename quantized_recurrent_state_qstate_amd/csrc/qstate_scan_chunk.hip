@@ -57,8 +57,10 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
   const int s = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
   const int h = hv / vchunks, v0 = (hv % vchunks) * kDV;
   const int kh = h / (a.H / a.G);
-  const Segment sg = find_segment(a, g.seg, s);
+  Segment sg = find_segment(a, g.seg, s);
+  if (OUT && !sg.none) outputs_of(sg, a, g, h);
   if (sg.none || (!OUT && sg.last)) return;
+  if (!OUT && sg.first && v0 == 0 && tid == 0) g.uncut[(int64_t)sg.seq * a.H + h] = 0;
   const int64_t head = (int64_t)h * a.dv;
 
   // state tiles: row 4 q4 + r of tile 2 i + j is channel 32 i + 8 q4 + 4 j + r, column m is value v0 + ...
@@ -154,7 +156,9 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
       const float e = __builtin_amdgcn_exp2f((float)c), w = __builtin_amdgcn_exp2f((float)(all - c));
       se[lane] = e;
       sw[lane] = w * nb;
-      if constexpr (OUT) sgrow = __ballot(e >= 0x1p100f || w >= 0x1p100f) != 0;
+      const bool grow = __ballot(e >= 0x1p100f || w >= 0x1p100f) != 0;
+      if constexpr (OUT) sgrow = grow;
+      else if (grow) total = NAN;            // the sequence is not cut
     }
     __syncthreads();
     const int next = t + n;
@@ -390,6 +394,7 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
   if (end <= start) return;
   const int c0 = start / g.seg, c1 = (end - 1) / g.seg;
+  bool numbers = true;
   F4* st = (F4*)g.states;
   F4 S = (F4){0, 0, 0, 0};
   if (a.initial) S = ((const F4*)a.initial)[(int64_t)seq * all + e];
@@ -416,8 +421,10 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
       st[(int64_t)(c + i + seq) * all + e] = S;   // what was there is in L
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[r] = fmaf(d[i][r], S[r], L[i][r]);
+      numbers &= finite(d[i]);
     }
   }
+  if (!numbers) g.uncut[(int64_t)seq * a.H + h] = 1;
   if (c1 > c0) st[(int64_t)(c1 + seq) * all + e] = S;
 }
 

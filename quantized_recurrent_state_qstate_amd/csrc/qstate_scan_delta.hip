@@ -209,8 +209,9 @@ struct Chunk {
 // values of zero, from the identity) into `carry`, k_delta_join goes from
 // piece to piece, and the OUT pass makes the outputs of all pieces at once.
 template <int DK, int WAVES, int VEC, bool OUT>
-__global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const float* prep, int cut, float* carry,
-                                                              int vchunks) {
+__global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, const ScanSegs g, int vchunks) {
+  const float* prep = g.states;
+  float* carry = g.total;
   constexpr int kDV = 16 * WAVES, kKS = DK / 32;
   using Buf = Chunk<DK, kDV>;
   constexpr bool kTwo = 2 * sizeof(Buf) + WAVES * kL * 32 <= 160 * 1024;   // room for two buffers
@@ -222,10 +223,12 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   const int per = a.H * (OUT ? vchunks : vchunks + DK / kDV);
   const int hv = (int)(blockIdx.x % (uint32_t)per), h = hv % a.H, kh = h / (a.H / a.G);
   const int part = (int)(blockIdx.x / (uint32_t)per);
-  const Piece piece_of = find_piece(a, cut, part);
+  Piece piece_of = find_piece(a, g.cut, part);
   const bool matrix = !OUT && hv / a.H >= vchunks;   // columns of M
   const int v0 = matrix ? 0 : hv / a.H * kDV, m0 = matrix ? (hv / a.H - vchunks) * kDV : 0;
+  if (OUT && !piece_of.none) outputs_of(piece_of, a, g, h);
   if (piece_of.none || (!OUT && (piece_of.last || (matrix && piece_of.first)))) return;
+  if (!OUT && piece_of.first && v0 == 0 && tid == 0) g.uncut[(int64_t)piece_of.seq * a.H + h] = 0;
   const int seq = piece_of.seq, start = piece_of.t0, end = piece_of.t1;
   const int64_t head = (int64_t)h * a.dv, st = (int64_t)seq * a.H * a.dv;
   const int col = wave * 16 + m, v = v0 + col;
@@ -523,7 +526,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
 // pieces of 2 heads of 128 x 128 take 35 us (87 without, by 16 rows).
 constexpr int kJoinRows = 8;
 template <int DK>
-__global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, float* carry, int rchunks) {
+__global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, const ScanSegs g, int rchunks) {
+  const int cut = g.cut;
+  float* carry = g.total;
   constexpr int kGroups = 512 / DK, kJ = DK / kGroups, kE = kJoinRows * DK / 512;
   __shared__ __attribute__((aligned(16))) float ss[kJoinRows][DK], sums[kGroups][kJoinRows * DK];
   const int tid = (int)threadIdx.x;
@@ -559,6 +564,7 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, f
     S[e] = in ? piece_at(c0)[(int64_t)r0 * DK + tid + 512 * e] : 0.0f;   // began with the initial state
     keep(c0, e, a.initial && in ? a.initial[at] : 0.0f);
   }
+  bool numbers = true;
   ask(c0 + 1);
   for (int c = c0 + 1; c < c1; ++c) {
     float next[kE];
@@ -584,6 +590,8 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, f
 #pragma unroll
       for (int r = 0; r < kJoinRows; ++r) asm volatile("" : "+v"(acc[r]) : : "memory");
     }
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) numbers &= fabsf(w[j]) < INFINITY;
     ask(min(c + 1, c1 - 1));
 #pragma unroll
     for (int r = 0; r < kJoinRows; ++r) sums[tid / DK][r * DK + ch] = acc[r];
@@ -597,12 +605,13 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, int cut, f
   }
 #pragma unroll
   for (int e = 0; e < kE; ++e) keep(c1, e, S[e]);
+  if (!numbers) g.uncut[(int64_t)seq * a.H + h] = 1;
 }
 
 template <int DK>
 hipError_t join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int rchunks = (a.dv + kJoinRows - 1) / kJoinRows;
-  k_delta_join<DK><<<dim3((uint32_t)(a.n * a.H * rchunks)), 512, 0, s>>>(a, g.cut, g.total, rchunks);
+  k_delta_join<DK><<<dim3((uint32_t)(a.n * a.H * rchunks)), 512, 0, s>>>(a, g, rchunks);
   return hipGetLastError();
 }
 
@@ -617,12 +626,11 @@ hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int pieces = a.n + (g.cut > 0 ? (a.T - 1) / g.cut : 0);
   if (g.cut > 0) {
     k_delta_scan<DK, WAVES, VEC, false><<<dim3((uint32_t)(pieces * a.H * (vchunks + DK / (16 * WAVES)))), 64 * WAVES, 0, s>>>(
-        a, g.states, g.cut, g.total, vchunks);
+        a, g, vchunks);
     const hipError_t e = join<DK>(a, g, s);
     if (e != hipSuccess) return e;
   }
-  k_delta_scan<DK, WAVES, VEC, true><<<dim3((uint32_t)(pieces * a.H * vchunks)), 64 * WAVES, 0, s>>>(
-      a, g.states, g.cut, g.total, vchunks);
+  k_delta_scan<DK, WAVES, VEC, true><<<dim3((uint32_t)(pieces * a.H * vchunks)), 64 * WAVES, 0, s>>>(a, g, vchunks);
   return hipGetLastError();
 }
 

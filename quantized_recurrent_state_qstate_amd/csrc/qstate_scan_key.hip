@@ -90,8 +90,10 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
   const int per = a.H * vchunks;
   const int s = (int)(blockIdx.x / (uint32_t)per), hv = (int)(blockIdx.x % (uint32_t)per);
   const int h = hv % a.H, v0 = hv / a.H * kDV, kh = h / (a.H / a.G);
-  const Segment sg = find_segment(a, g.seg, s);
+  Segment sg = find_segment(a, g.seg, s);
+  if (OUT && !sg.none) outputs_of(sg, a, g, h);
   if (sg.none || (!OUT && sg.last)) return;
+  if (!OUT && sg.first && v0 == 0 && tid == 0) g.uncut[(int64_t)sg.seq * a.H + h] = 0;
   const int64_t head = (int64_t)h * a.dv;
   const float skip = a.skip ? a.skip[h] : 0.0f;
 
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
     const int n = min(kB, sg.t1 - t);
     // ---- products of the decays within 4 tokens
     float pre[4][kC], suf[4][kC];
-    bool bad = odd(largest((H2){0, 0}, nv));
+    bool bad = OUT && odd(largest((H2){0, 0}, nv));
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       pre[0][j] = nd[0][j];
@@ -200,7 +202,9 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
           const float inv = __builtin_amdgcn_rcpf(D);     // within 1 ulp; one Newton step
           y[j] = kb * fmaf(fmaf(-D, inv, 1.0f), inv, inv);
         }
-        z[j] = kb * (suf[i][j] * behind[j]);
+        const float rest = suf[i][j] * behind[j];
+        if constexpr (!OUT) bad |= !(D <= 0x1p100f && rest <= 0x1p100f);
+        z[j] = kb * rest;
       }
       if constexpr (OUT) {
         put_pieces<kC>(&sq[0][r * kR + ch], kB * kR, x);
@@ -208,10 +212,13 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
       }
       put_pieces<kC>(&su[0][r * kR + ch], kB * kR, z);
     }
-    if (OUT && (bad || far > 120u << 23 || high > 100 << 23 || low < 154u << 23)) sodd[turn] = 1;
+    if (bad || (OUT && (far > 120u << 23 || high > 100 << 23 || low < 154u << 23))) sodd[turn] = 1;
     if (tid == 0) sodd[turn ^ 1] = 0;        // read in the block before, next written in the next
     __syncthreads();
     if (t + kB < sg.t1) fetch(t + kB);
+    if (!OUT && sodd[turn])                  // decays that grow out of fp32: the sequence is not cut
+#pragma unroll
+      for (int j = 0; j < kC; ++j) whole[j] = NAN;
     if (OUT && sodd[turn]) {
       // ---- token by token, q, k and the decays from memory
 #pragma unroll

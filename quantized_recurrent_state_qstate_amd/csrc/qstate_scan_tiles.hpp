@@ -89,6 +89,7 @@ __device__ __forceinline__ double wave_sums(double x) {
 struct Segment {
   int seq, t0, t1;      // tokens
   bool first, last, none;
+  int end;              // the sequence's
 };
 // The last sequence i > 0 with `le(i)`, which holds up to some i and not behind; else 0.
 template <class F>
@@ -105,7 +106,7 @@ __device__ __forceinline__ int last_sequence(const ScanArgs& a, F le) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int s) {
-  Segment r{0, 0, 0, true, true, false};
+  Segment r{0, 0, 0, true, true, false, 0};
   int start = 0, end = a.T;
   if (a.offsets) {
     r.seq = last_sequence(a, [&](int i) { return min(max(a.offsets[i], 0), a.T) / seg + i <= s; });
@@ -118,6 +119,7 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
   r.last = c == c1;
   r.t0 = r.first ? start : c * seg;
   r.t1 = r.last ? end : (c + 1) * seg;
+  r.end = end;
   return r;
 }
 
@@ -132,6 +134,7 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
 struct Piece {
   int seq, t0, t1;
   bool first, last, none;
+  int end;
 };
 __device__ __forceinline__ bool long_enough(int start, int end, int cut) { return cut > 0 && (end - start + 1) / 2 > cut; }
 __device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
@@ -140,8 +143,23 @@ __device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
   const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
   const bool many = long_enough(start, end, cut);
-  if (s < a.n) return {seq, start, many ? (start / cut + 1) * cut : end, true, !many, false};
-  return {seq, x, min(x + cut, end), false, x + cut >= end, !(many && start < x && x < end)};
+  if (s < a.n) return {seq, start, many ? (start / cut + 1) * cut : end, true, !many, false, end};
+  return {seq, x, min(x + cut, end), false, x + cut >= end, !(many && start < x && x < end), end};
+}
+
+// A sequence that is cut needs its segments' whole decays (the delta rule's M) to
+// be numbers: decays above one may leave fp32 where the state, zero or small, does
+// not.  Where one is not, the join says so for that head, and the outputs are made
+// in one piece: by the workgroups of the first one, which take the whole sequence.
+template <class P>
+__device__ __forceinline__ void outputs_of(P& p, const ScanArgs& a, const ScanSegs& g, int h) {
+  if ((p.first && p.last) || !g.uncut[(int64_t)p.seq * a.H + h]) return;
+  p.none |= !p.first;
+  p.t1 = p.end;
+  p.last = true;
+}
+__device__ __forceinline__ bool finite(F4 x) {
+  return fabsf(x[0]) < INFINITY && fabsf(x[1]) < INFINITY && fabsf(x[2]) < INFINITY && fabsf(x[3]) < INFINITY;
 }
 
 // 16 bytes a lane from a buffer at `offset` to LDS, lane after lane from `to` on

@@ -210,6 +210,13 @@ int main() {
               const uint64_t per = g_chunked == 3 ? (uint64_t)qs::kScanPrepBytes : 64ull * 128 * 4;
               CHECK((char*)g_segs.states + (uint64_t)g_segs.count * 8 * per <= at(6000ull << 32) + need);
             }
+            if (g_segs.states ? g_chunked != 3 : g_segs.cut > 0)
+              CHECK(g_segs.uncut != nullptr);
+            if (g_segs.uncut) {                       // a word for each head of a sequence, behind all else
+              const uint64_t per = g_chunked == 3 ? (uint64_t)qs::kScanPrepBytes : 64ull * 128 * 4;
+              CHECK((char*)(g_segs.uncut + (int64_t)n * 8) <= at(6000ull << 32) + need);
+              if (g_segs.states) CHECK((char*)g_segs.states + (uint64_t)g_segs.count * 8 * per <= (char*)g_segs.uncut);
+            }
             if (g_segs.cut > 0) {                     // pieces: L and M in front of the prepared chunks
               const uint64_t pieces = (uint64_t)((T - 1) / g_segs.cut + n);
               CHECK((char*)g_segs.total + pieces * 8 * (64 + 128) * 128 * 4 <=

@@ -103,10 +103,8 @@ def test_scan_overflowing_sum_before_its_decay():
     right("additive", "bf16", a, *scan("additive", "head", "bf16", a, initial=S0), initial=S0)
 
 
-GROWING = [("additive", "head", "bf16"), ("delta", "head", "bf16")]
-
-
-@pytest.mark.parametrize("kind,decay,dtype", GROWING)
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_scan_growing_decays_of_nothing(kind, decay, dtype):
     """Decays above one whose product leaves fp32, while the state is still zero."""
     a = make(kind, decay, 130, 2, 1, 64, 48, dtype)
@@ -116,7 +114,8 @@ def test_scan_growing_decays_of_nothing(kind, decay, dtype):
     right(kind, dtype, a, *scan(kind, decay, dtype, a))
 
 
-@pytest.mark.parametrize("kind,decay,dtype", GROWING)
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_scan_growing_decays_of_little(kind, decay, dtype):
     """... or so small that the product with it is not large."""
     a = make(kind, decay, 130, 2, 1, 64, 48, dtype)
@@ -125,3 +124,19 @@ def test_scan_growing_decays_of_little(kind, decay, dtype):
     a["v"][24:30] = 0
     a["decay"][24:30] = 2.0 ** -6
     right(kind, dtype, a, *scan(kind, decay, dtype, a))
+
+
+@pytest.mark.parametrize("kind,decay", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lengths", [[4096], [100, 3000, 0, 996]])
+def test_scan_growing_decays_over_segments(kind, decay, dtype, lengths):
+    """Whole segments and pieces whose decays leave fp32, with a state of zero before and in them, then ordinary
+    tokens; one head of the two is ordinary throughout."""
+    T = sum(lengths)
+    a = make(kind, decay, T, 2, 1, 64, 48, dtype, mu=5.0)
+    quiet = slice(100, 2600)
+    a["decay"][quiet, 0] = 8.0
+    a["v"][quiet, 0] = 0
+    if len(lengths) == 1:
+        a["v"][:100, 0] = 0
+    right(kind, dtype, a, *scan(kind, decay, dtype, a, lengths), lengths=lengths)
