@@ -95,7 +95,6 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
   const bool matrix = DELTA && !OUT && rc >= rchunks;   // rows of M
   if (OUT && !seg.none) outputs_of(seg, a, gs, h);
   if (seg.none || (!OUT && (seg.last || (matrix && seg.first)))) return;
-  if (!OUT && seg.first && rc == 0 && threadIdx.x == 0) gs.uncut[(int64_t)seg.seq * a.H + h] = 0;
   const int t0 = seg.t0, t1 = seg.t1;
   const int sub = tid & 15, row = (tid >> 4) * RPL;   // this lane's channels and first row
   const int r0 = (matrix ? rc - rchunks : rc) * kRows, rows = matrix ? DK : a.dv;
@@ -267,6 +266,7 @@ __global__ __launch_bounds__(256) void k_scan(const ScanArgs a, const ScanSegs g
         for (int m = 0; m < kM; ++m)
           *(float4*)(to + (int64_t)(r0 + row + r) * DK + m * 64 + sub * 4) =
               make_float4(s[r][m][0], s[r][m][1], s[r][m][2], s[r][m][3]);
+  if (!OUT && seg.first && rc == 0 && tid == 0) gs.uncut[(int64_t)seg.seq * a.H + h] = 0;   // until the join finds otherwise
   if (!OUT && !DELTA && rc == 0 && tid < 16) {
     if constexpr (KEY) {
 #pragma unroll

@@ -60,7 +60,6 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
   Segment sg = find_segment(a, g.seg, s);
   if (OUT && !sg.none) outputs_of(sg, a, g, h);
   if (sg.none || (!OUT && sg.last)) return;
-  if (!OUT && sg.first && v0 == 0 && tid == 0) g.uncut[(int64_t)sg.seq * a.H + h] = 0;
   const int64_t head = (int64_t)h * a.dv;
 
   // state tiles: row 4 q4 + r of tile 2 i + j is channel 32 i + 8 q4 + 4 j + r, column m is value v0 + ...
@@ -379,7 +378,10 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
           *(F4*)(to + (head + col) * DK + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1)) = S[v][t];
     }
   }
-  if (!OUT && tid == 0 && v0 == 0) g.total[(int64_t)s * a.H + h] = __builtin_amdgcn_exp2f((float)total);
+  if (!OUT && tid == 0 && v0 == 0) {
+    g.total[(int64_t)s * a.H + h] = __builtin_amdgcn_exp2f((float)total);
+    if (sg.first) g.uncut[(int64_t)sg.seq * a.H + h] = 0;   // until the join finds otherwise
+  }
 }
 
 // States between segments: for each sequence, S = initial, then S = decay S + local

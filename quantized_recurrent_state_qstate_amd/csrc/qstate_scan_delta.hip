@@ -52,7 +52,7 @@ static_assert(kPrepFloats * 4 == kScanPrepBytes, "workspace a chunk and head");
 __device__ __forceinline__ int piece(int i, int c) { return i < 2 ? i : 2 * i - 2 + c; }
 
 template <int DK, bool VEC>
-__global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* prep) {
+__global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* prep, int32_t* uncut) {
   constexpr int kKS = DK / 32, kKR = DK + 8, kAR = kL + 4, kKP = kL * DK / 8 / 256;
   __shared__ __attribute__((aligned(16))) uint16_t sk[kL * kKR], sq[kL * kKR];
   __shared__ __attribute__((aligned(16))) float sa[kL * kAR];   // minus A; then T
@@ -69,6 +69,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const ScanArgs a, float* pre
   const Tile<VEC> tk(a.k, (int64_t)sg.t0 * a.ks + (int64_t)kh * DK, a.ks, n, DK);
   const Tile<VEC> tq(a.q, (int64_t)sg.t0 * a.qs + (int64_t)kh * DK, a.qs, n, DK);
   if (tid == 0) sodd = 0.0f;
+  if (uncut && sg.first && tid == 0) uncut[(int64_t)sg.seq * a.H + h] = 0;   // until the join finds otherwise
   __syncthreads();
   H2 most = (H2){0, 0};
 #pragma unroll
@@ -228,7 +229,6 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_delta_scan(const ScanArgs a, 
   const int v0 = matrix ? 0 : hv / a.H * kDV, m0 = matrix ? (hv / a.H - vchunks) * kDV : 0;
   if (OUT && !piece_of.none) outputs_of(piece_of, a, g, h);
   if (piece_of.none || (!OUT && (piece_of.last || (matrix && piece_of.first)))) return;
-  if (!OUT && piece_of.first && v0 == 0 && tid == 0) g.uncut[(int64_t)piece_of.seq * a.H + h] = 0;
   const int seq = piece_of.seq, start = piece_of.t0, end = piece_of.t1;
   const int64_t head = (int64_t)h * a.dv, st = (int64_t)seq * a.H * a.dv;
   const int col = wave * 16 + m, v = v0 + col;
@@ -590,8 +590,10 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, const Scan
 #pragma unroll
       for (int r = 0; r < kJoinRows; ++r) asm volatile("" : "+v"(acc[r]) : : "memory");
     }
+    float zero = 0.0f;                      // or NaN
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) numbers &= fabsf(w[j]) < INFINITY;
+    for (int j = 0; j < kJ; ++j) zero = fmaf(w[j], 0.0f, zero);
+    numbers &= zero == 0.0f;
     ask(min(c + 1, c1 - 1));
 #pragma unroll
     for (int r = 0; r < kJoinRows; ++r) sums[tid / DK][r * DK + ch] = acc[r];
@@ -622,7 +624,7 @@ hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   // in all; sixteen of 256: 107, 172).
   constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
-  k_delta_prep<DK, (VEC > 0)><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states);
+  k_delta_prep<DK, (VEC > 0)><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states, g.uncut);
   const int pieces = a.n + (g.cut > 0 ? (a.T - 1) / g.cut : 0);
   if (g.cut > 0) {
     k_delta_scan<DK, WAVES, VEC, false><<<dim3((uint32_t)(pieces * a.H * (vchunks + DK / (16 * WAVES)))), 64 * WAVES, 0, s>>>(

@@ -93,7 +93,6 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
   Segment sg = find_segment(a, g.seg, s);
   if (OUT && !sg.none) outputs_of(sg, a, g, h);
   if (sg.none || (!OUT && sg.last)) return;
-  if (!OUT && sg.first && v0 == 0 && tid == 0) g.uncut[(int64_t)sg.seq * a.H + h] = 0;
   const int64_t head = (int64_t)h * a.dv;
   const float skip = a.skip ? a.skip[h] : 0.0f;
 
@@ -350,6 +349,7 @@ __global__ __launch_bounds__(256, DK <= 128 && VEC > 0 ? 2 : 1) void k_scan_key(
   if (!OUT && wave == 0 && v0 == 0)
 #pragma unroll
     for (int j = 0; j < kC; ++j) g.total[((int64_t)s * a.H + h) * DK + ch + j] = whole[j];
+  if (!OUT && tid == 0 && v0 == 0 && sg.first) g.uncut[(int64_t)sg.seq * a.H + h] = 0;   // until the join finds otherwise
 }
 
 template <int DK, int NV, int VEC>

@@ -153,7 +153,7 @@ __device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
 // in one piece: by the workgroups of the first one, which take the whole sequence.
 template <class P>
 __device__ __forceinline__ void outputs_of(P& p, const ScanArgs& a, const ScanSegs& g, int h) {
-  if ((p.first && p.last) || !g.uncut[(int64_t)p.seq * a.H + h]) return;
+  if ((p.first && p.last) || !__builtin_amdgcn_readfirstlane(g.uncut[(int64_t)p.seq * a.H + h])) return;
   p.none |= !p.first;
   p.t1 = p.end;
   p.last = true;
