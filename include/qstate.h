@@ -308,7 +308,8 @@ qs_status qstate_causal_conv_step(const qstate_conv* c, void* stream);
 typedef enum { QS_NORM_NONE = 0, QS_NORM_L2 = 1, QS_NORM_RMS = 2 } qs_norm;
 
 /* Norm of each query and key head and the rotation by position, in one pass:
- *   L2:  y = x / sqrt(sum x^2 + eps);  RMS: y = x / sqrt(mean x^2 + eps) * weight;
+ *   L2:  y = x / sqrt(sum x^2 + eps);  RMS: y = x / sqrt(mean x^2 + eps) * weight
+ *   (heads whose squares leave fp32 included; eps = 0 and a head of zeros: NaN);
  *   pairs of y's first `rot` channels turn by position * frequency[pair]:
  *   (a, b) -> (a cos - b sin, a sin + b cos), pairs (i, i + rot/2), or
  *   (2i, 2i+1) when interleaved;  q_out = y q_scale, k_out = y.

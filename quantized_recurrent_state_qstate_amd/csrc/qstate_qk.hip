@@ -100,16 +100,23 @@ __global__ __launch_bounds__(256) void k_qk(const QkArgs a, int splits, int per)
 #pragma unroll
       for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
       float inv = 1.0f / sqrtf((a.norm == 2 ? ss / (float)a.dim : ss) + a.eps);
-      if (__ballot(ss > 0x1p126f)) {       // squares beyond fp32: again with x 2^-70, where eps is nothing
+      // Squares beyond fp32, or (where eps is not above what they could add) subnormal
+      // ones: again with x 2^-70, where eps is nothing, or x 2^100.
+      const bool large = ss > 0x1p126f, tiny = a.eps < 0x1p-70f && ss < 0x1p-100f;
+      if (__ballot(large || tiny)) {
+        const float by = large ? 0x1p-70f : tiny ? 0x1p100f : 1.0f;
         float s2 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s2 = fmaf(f[j] * 0x1p-70f, f[j] * 0x1p-70f, s2);
+        for (int j = 0; j < 8; ++j) {
+          const float x = f[j] * by;
+          s2 = fmaf(x, x, s2);
+        }
 #pragma unroll
         for (int m = 1; m < L; m <<= 1) s2 += __shfl_xor(s2, m);
-        if (ss > 0x1p126f) {
-          inv = 1.0f / sqrtf(a.norm == 2 ? s2 / (float)a.dim : s2);
+        if (large || tiny) {
+          inv = 1.0f / sqrtf((a.norm == 2 ? s2 / (float)a.dim : s2) + a.eps * by * by);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] *= 0x1p-70f;
+          for (int j = 0; j < 8; ++j) f[j] *= by;
         }
       }
 #pragma unroll

@@ -106,7 +106,8 @@ def qk_norm_rotate(q, k=None, *, norm="l2", q_weight=None, k_weight=None, eps=1e
     q [T, Hq, d], k [T, Hk, d] or None, bf16 or fp32, d a multiple of 8 up to
     512; the rows may lie in a wider tensor if each starts 16-byte aligned.
     norm: "l2" (x / sqrt(sum x^2 + eps)), "rms" (x / sqrt(mean x^2 + eps),
-    times q_weight / k_weight fp32 [d] if given) or "none".
+    times q_weight / k_weight fp32 [d] if given) or "none"; a head of zeros
+    with eps 0 gives NaN.
     frequency fp64 [rot/2] (radians per position) with position int32 [T]:
     the first `rot` channels turn, in pairs (i, i + rot/2), or (2i, 2i+1) when
     interleaved.  q_scale multiplies q_out.  q_out may be q, k_out may be k."""
