@@ -128,6 +128,24 @@ def check_tensor(name: str, t, dtype, numel: int, device, at_least: bool = False
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
+def check_states(name: str, t, dtype, shape, device) -> None:
+    """States of shape [n,H,dv,dk], or with neighbouring dimensions as one: another
+    order of them (keys first) has as many elements."""
+    numel = shape[0] * shape[1] * shape[2] * shape[3]
+    check_tensor(name, t, dtype, numel, device)
+    if t.shape == shape or not numel:
+        return
+    inner, whole = {1}, 1
+    for size in reversed(shape):
+        whole *= size
+        inner.add(whole)
+    whole = 1
+    for size in reversed(t.shape):
+        whole *= size
+        if whole not in inner:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
 def check_state(cfg: "StateConfig", sizes: dict, st: dict, device) -> None:
     """Every buffer the plan sizes > 0 must be present, typed and large enough."""
     import torch
@@ -367,7 +385,7 @@ class QState:
         if skip is not None:
             check_tensor("skip", skip, f32, H, dev)
         if initial is not None:
-            check_tensor("initial", initial, f32, n * H * dv * dk, dev)
+            check_states("initial", initial, f32, (n, H, dv, dk), dev)
         if out is None:
             out = _empty_like(v, vs == H * dv, stream)
             os = H * dv
@@ -376,7 +394,7 @@ class QState:
         if final is None:
             final = _empty((n, H, dv, dk), f32, dev, stream)
         else:
-            check_tensor("final", final, f32, n * H * dv * dk, dev)
+            check_states("final", final, f32, (n, H, dv, dk), dev)
         a = _lib.Scan(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(beta), _ptr(skip),
                       _ptr(initial), final.data_ptr(), out.data_ptr(), _ptr(offsets), qs, ks, vs, ds, bs, os, T, n, G)
         L = _lib.lib()

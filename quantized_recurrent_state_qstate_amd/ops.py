@@ -52,6 +52,8 @@ def _conv(x, weight, bias, window, slot, n, silu, out, stream):
             raise ValueError("window must be [slots, W-1, C]")
         slots = window.shape[0]
         check_tensor("window", window, dtype, slots * (W - 1) * C, dev)
+        if window.shape != (slots, W - 1, C):
+            raise ValueError(f"window: shape {tuple(window.shape)}, expected {(slots, W - 1, C)}")
     if slot is not None:
         check_tensor("slot", slot, torch.int32, n, dev)
     if out is None:

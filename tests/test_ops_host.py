@@ -180,3 +180,30 @@ def test_the_pool_as_its_own_source_has_no_more_slots(m):
     idx = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="state\\['codes'\\]: .* expected at least"):
         qs.copy_slots(pool, idx, idx, source=pool, source_slots=m)
+
+
+def test_windows_and_states_of_another_layout_are_refused():
+    """The right number of elements in the wrong order of dimensions."""
+    x, w = torch.zeros(10, 32), torch.zeros(4, 32)
+    off, slot = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for window in (torch.zeros(3, 32, 3), torch.zeros(3, 3, 16, 2), torch.zeros(3, 96), torch.zeros(3, 1, 96)):
+        with pytest.raises(ValueError, match="window"):
+            causal_conv(x, w, offsets=off, window=window, slot=slot)
+        with pytest.raises(ValueError, match="window"):
+            causal_conv_step(x[:2], w, window=window, slot=slot)
+    with pytest.raises(ValueError, match="expected a GPU"):       # nothing else was wrong
+        causal_conv(x, w, offsets=off, window=torch.zeros(3, 3, 32), slot=slot)
+    for bad in (torch.zeros(32, 4), torch.zeros(128), torch.zeros(4, 32, 1)):
+        with pytest.raises(ValueError, match="weight"):
+            causal_conv(x, bad, offsets=off)
+    qs = handle(kind="delta", B=2, H=4, dk=64, dv=32)
+    T, bf = 6, torch.bfloat16
+    args = dict(q=torch.zeros(T, 2, 64, dtype=bf), k=torch.zeros(T, 2, 64, dtype=bf), v=torch.zeros(T, 4, 32, dtype=bf),
+                decay=torch.zeros(T, 4), offsets=off)
+    for name in ("initial", "final"):
+        for shape in ((2, 4, 64, 32), (4, 2, 32, 64), (2, 32, 4, 64), (8, 64, 32), (2, 64, 4, 32), (64, 256)):
+            with pytest.raises(ValueError, match=f"{name}: shape"):
+                qs.scan(**args, **{name: torch.zeros(shape)})
+        for shape in ((2, 4, 32, 64), (8, 32, 64), (2, 4, 2048), (2 * 4 * 32 * 64,), (1, 2, 4, 32, 64)):
+            with pytest.raises(_lib.QStateError, match="handle is NULL"):    # as far as the library
+                qs.scan(**args, **{name: torch.zeros(shape)})
