@@ -371,7 +371,8 @@ qs_status qstate_scan_workspace(const qstate_handle* h, const qstate_scan_args* 
 
 /* `workspace`: device memory of at least that size, 256-byte aligned, used
  * by this call alone until it has finished on `stream` (NULL when 0 bytes).
- * Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
+ * Calls whose launches would have 2^32 threads (from about 2^29 value rows of
+ * all sequences on) are refused.  Errors: QS_EINVAL, QS_EUNSUPPORTED, QS_EHIP. */
 qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* a, void* workspace, uint64_t bytes,
                       void* stream);
 

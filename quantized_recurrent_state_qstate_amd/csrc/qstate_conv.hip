@@ -71,11 +71,11 @@ __device__ __forceinline__ int find_seq(const int32_t* off, int n, int t) {
 constexpr int kRows = 4;   // tokens a thread has in registers at a time; the next ones are on their way
 
 // Blocks [0, tiles): runs of kRows * steps tokens x 64*V channels a wave.  The
-// other blocks: one sequence x 256*V channels: its first W-1 outputs, which
-// read the window, and the new window.  Only they touch the window, so no
-// block waits for another.
+// other blocks: one sequence (from seq0 on) x 256*V channels: its first W-1
+// outputs, which read the window, and the new window.  Only they touch the
+// window, so no block waits for another.
 template <int BF16, int V, int W>
-__global__ __launch_bounds__(256) void k_conv(const ConvArgs a, int ctiles, int tiles, int sctiles, int steps) {
+__global__ __launch_bounds__(256) void k_conv(const ConvArgs a, int ctiles, int tiles, int sctiles, int steps, int seq0) {
   using E = typename Elem<BF16>::type;
   using VT = typename Vec<BF16, V>::type;
   const E* x = (const E*)a.x;
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void k_conv(const ConvArgs a, int ctiles, int 
   }
   // one sequence's beginning and its window
   const int sb = b - tiles;
-  const int seq = sb / sctiles;
+  const int seq = seq0 + sb / sctiles;
   const int c = ((sb % sctiles) * 256 + (int)threadIdx.x) * V;
   if (c >= a.C) return;
   const int sl = a.slot ? a.slot[seq] : seq;
@@ -232,10 +232,10 @@ __global__ __launch_bounds__(256) void k_conv(const ConvArgs a, int ctiles, int 
 // One token of each of n sequences: a thread holds V channels of one sequence,
 // reads the window and the token, writes the output and the shifted window.
 template <int BF16, int V, int W>
-__global__ __launch_bounds__(64) void k_conv_step(const ConvArgs a, int ctiles) {
+__global__ __launch_bounds__(64) void k_conv_step(const ConvArgs a, int ctiles, int seq0) {
   using E = typename Elem<BF16>::type;
   using VT = typename Vec<BF16, V>::type;
-  const int seq = (int)blockIdx.x / ctiles;
+  const int seq = seq0 + (int)blockIdx.x / ctiles;
   const int c = (((int)blockIdx.x % ctiles) * 64 + (int)threadIdx.x) * V;
   if (c >= a.C) return;
   const int sl = a.slot ? a.slot[seq] : seq;
@@ -266,19 +266,34 @@ hipError_t conv(const ConvArgs& a, hipStream_t s) {
   // step, 182 with four, 178 with eight, 198 with sixteen and a quarter of the waves).
   int steps = 1;
   while (steps < 8 && (int64_t)ctiles * (a.T / (kRows * 2 * steps)) >= 8192) steps *= 2;
-  const int tiles = ctiles * (int)(((int64_t)a.T + 4 * kRows * steps - 1) / (4 * kRows * steps));
+  auto runs = [&] { return ctiles * (((int64_t)a.T + 4 * kRows * steps - 1) / (4 * kRows * steps)); };
+  while (runs() > max_blocks(256) / 2) steps *= 2;
   const int sctiles = (a.C + 256 * V - 1) / (256 * V);
-  const int64_t blocks = (int64_t)tiles + (a.window ? (int64_t)a.n * sctiles : 0);
-  if (blocks == 0) return hipSuccess;
-  k_conv<BF16, V, W><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, ctiles, tiles, sctiles, steps);
-  return hipGetLastError();
+  const int64_t most = max_blocks(256) / 2 / sctiles;   // sequences of a launch
+  int64_t tiles = runs(), seq = 0;
+  do {
+    const int64_t n = !a.window ? 0 : a.n - seq < most ? a.n - seq : most;
+    if (tiles + n == 0) break;
+    k_conv<BF16, V, W><<<dim3((uint32_t)(tiles + n * sctiles)), 256, 0, s>>>(a, ctiles, (int)tiles, sctiles, steps, (int)seq);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    tiles = 0;
+    seq += n;
+  } while (a.window && seq < a.n);
+  return hipSuccess;
 }
 
 template <int BF16, int V, int W>
 hipError_t conv_step(const ConvArgs& a, hipStream_t s) {
   const int ctiles = (a.C + 64 * V - 1) / (64 * V);
-  k_conv_step<BF16, V, W><<<dim3((uint32_t)(a.n * ctiles)), 64, 0, s>>>(a, ctiles);
-  return hipGetLastError();
+  const int64_t most = max_blocks(64) / ctiles;         // sequences of a launch
+  for (int64_t seq = 0; seq < a.n; seq += most) {
+    const int64_t n = a.n - seq < most ? a.n - seq : most;
+    k_conv_step<BF16, V, W><<<dim3((uint32_t)(n * ctiles)), 64, 0, s>>>(a, ctiles, (int)seq);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 #define QS_CONV_PICK(fn)                                                        \

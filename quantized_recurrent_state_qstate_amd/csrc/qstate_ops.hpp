@@ -22,6 +22,11 @@ HandleView op_view(const qstate_handle* h);
 qs_status op_check_tensors(const qstate_handle* h, const qstate_tensors* st);
 qs_status op_check_device(const qstate_handle* h);
 
+// A launch has fewer than 2^32 threads: the runtime takes the number modulo
+// 2^32, silently unless it is 0.  Launchers split what needs more, or their host
+// code refuses it.
+constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+
 // ---- short causal convolution ---------------------------------------------
 struct ConvArgs {
   const void* x;

@@ -92,7 +92,7 @@ qs_status check_conv(const qstate_conv* c, bool step, qs::ConvArgs* a) {
   // workgroups of the narrowest variant
   const int64_t tiles = (C + 63) / 64;
   const int64_t blocks = tiles * (step ? rows : rows / 16 + 1 + c->n);
-  if (blocks > 0x7FFFFFFF) return op_fail(QS_EUNSUPPORTED, "%lld rows of %lld channels in one call", (long long)rows, (long long)C);
+  if (blocks > 0x7FFFFFFF || tiles > qs::max_blocks(256) / 2) return op_fail(QS_EUNSUPPORTED, "%lld rows of %lld channels in one call", (long long)rows, (long long)C);
   return QS_OK;
 }
 
@@ -336,8 +336,11 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
     if (p.states) p.segs.states = (float*)((char*)workspace + p.total);
     if (p.uncut) p.segs.uncut = (int32_t*)((char*)workspace + p.total + p.states);
   }
-  if ((int64_t)p.segs.count * a.H * ((a.dv + 31) / 32) > 0x7FFFFFFF ||
-      (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > 0x7FFFFFFF)
+  // workgroups of 256 threads of the launches that have most: a segment's rows
+  // (by the delta rule M's too), and the joins
+  const int64_t blocks = (int64_t)std::max(p.segs.count, p.segs.cut ? a.n + (a.T - 1) / p.segs.cut : 0) * a.H;
+  if (blocks * ((a.dv + 31) / 32 + (p.segs.cut ? a.dk / 32 : 0)) > qs::max_blocks(256) ||
+      (int64_t)a.n * (((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256) > qs::max_blocks(256))
     return op_fail(QS_EUNSUPPORTED, "%d tokens of %d sequences in one call", a.T, a.n);
   a.q = c->q;
   a.k = c->k;
@@ -407,7 +410,7 @@ static qs_status slot_buffers(const qstate_handle* h, const qstate_tensors* pool
                                                       (unsigned long long)extra[i].bytes);
     add(extra[i].src, extra[i].dst, extra[i].bytes);
   }
-  if (pieces > 0x7FFFFFFF) return op_fail(QS_EUNSUPPORTED, "a slot of %llu pieces", (unsigned long long)pieces);
+  if (pieces > (uint64_t)qs::max_blocks(256)) return op_fail(QS_EUNSUPPORTED, "a slot of %llu pieces", (unsigned long long)pieces);
   a->pieces = (uint32_t)pieces;
   return QS_OK;
 }

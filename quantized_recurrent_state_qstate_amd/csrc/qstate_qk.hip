@@ -177,8 +177,21 @@ hipError_t qk(const QkArgs& a, hipStream_t s) {
   while (a.T * splits < 512 && (nh + splits - 1) / splits > round) splits *= 2;
   const int per = ((nh + splits - 1) / splits + round - 1) / round * round;
   splits = (nh + per - 1) / per;
-  k_qk<BF16, L><<<dim3((uint32_t)(a.T * splits)), 256, 0, s>>>(a, splits, per);
-  return hipGetLastError();
+  const int64_t most = max_blocks(256) / splits, es = BF16 ? 2 : 4;   // tokens of a launch
+  for (int64_t t = 0; t < a.T; t += most) {
+    QkArgs part = a;
+    part.T = (int32_t)(a.T - t < most ? a.T - t : most);
+    for (int i = 0; i < 2; ++i) {
+      if (!a.heads[i]) continue;
+      part.x[i] = (const char*)a.x[i] + t * a.xs[i] * es;
+      part.y[i] = (char*)a.y[i] + t * a.ys[i] * es;
+    }
+    if (a.position) part.position = a.position + t;
+    k_qk<BF16, L><<<dim3((uint32_t)(part.T * splits)), 256, 0, s>>>(part, splits, per);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

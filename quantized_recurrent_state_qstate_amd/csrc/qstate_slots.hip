@@ -117,8 +117,17 @@ __global__ __launch_bounds__(256) void k_compact_slots(const SlotArgs a) {
 }  // namespace
 
 hipError_t launch_copy_slots(const SlotArgs& a, hipStream_t s) {
-  k_copy_slots<<<dim3((uint32_t)a.n * a.pieces), 256, 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t most = max_blocks(256) / a.pieces;   // copies of a launch; the host refuses slots of more pieces
+  for (int64_t i = 0; i < a.n; i += most) {
+    SlotArgs part = a;
+    part.n = (int32_t)(a.n - i < most ? a.n - i : most);
+    part.src_slot = a.src_slot + i;
+    part.dst_slot = a.dst_slot + i;
+    k_copy_slots<<<dim3((uint32_t)part.n * a.pieces), 256, 0, s>>>(part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_compact_slots(const SlotArgs& a, hipStream_t s) {

@@ -224,6 +224,16 @@ int main() {
             }
           }
         }
+        // a launch has fewer than 2^32 threads
+        for (int n : {1 << 20, 1 << 21, 1 << 22}) {
+          a = scan_args(c, 100, n, 1);
+          a.final = (float*)at(5000ull << 32);
+          a.initial = nullptr;
+          const int before = g_launches;
+          const qs_status s = qstate_scan(h, &a, at(6000ull << 32), 1ull << 44, nullptr);
+          CHECK(s == ((int64_t)n * 8 * (64 * 128 / 1024) < (1 << 24) ? QS_OK : QS_EUNSUPPORTED));
+          CHECK(g_launches - before == (s == QS_OK));
+        }
         // slots
         qstate_sizes z;
         CHECK(qstate_plan(&c, &z) == QS_OK);
