@@ -94,6 +94,7 @@ struct ScanArgs {
   const int32_t* offsets;  // [n+1] or null (one sequence of T tokens)
   int64_t qs, ks, vs, ds, bs, os;   // elements between tokens
   int32_t T, n, H, G, dk, dv;
+  int32_t least, most;     // a launch takes the sequences of least .. most tokens, and leaves the others alone
   int32_t bf16, delta, key;
   int32_t vec;             // 16-byte accesses: 2 to q, k, v and out rows, 1 to q and k, 0 to none
 };

@@ -207,14 +207,17 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
   a->bf16 = f.in_dtype == QS_BF16;
   a->delta = f.kind == QS_KIND_DELTA;
   a->key = f.decay_mode == QS_DECAY_KEY;
+  a->least = 0;
+  a->most = 0x7FFFFFFF;
   return QS_OK;
 }
 
-// How a scan runs.  The chunked kernels take bf16 prompts but the delta rule
-// with a decay for every key channel, if the sequences are long enough on the
-// average: one sequence of 16 tokens, 32 heads of 128 x 128, takes 7.4 us
-// against 8.1 token by token (one of 8: 7.4, 6.1), sixteen of 64 by the delta
-// rule 71 against 90 us (of 32: 68, 50).  Everything else runs token by token.
+// How a scan's sequences run (a.least > 0: the long ones of them).  The chunked
+// kernels take bf16 prompts but the delta rule with a decay for every key channel,
+// if the sequences are long enough on the average: one of 16 tokens, 32 heads of
+// 128 x 128, takes 7.4 us against 8.1 token by token (one of 8: 7.4, 6.1), sixteen
+// of 64 by the delta rule 71 against 90 us (of 32: 68, 50).  Everything else runs
+// token by token.
 // Additive sequences are cut into segments when the heads alone would leave
 // compute units idle; a segment costs a state written, read and written again,
 // so it has at least 256 tokens (one decay a head; 16384 tokens of 32 heads of
@@ -224,7 +227,7 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
 // token by token, 64 (fp32, 2048 tokens of 8 heads of 64 x 64: 53 us, 62 with
 // at least 128, 464 uncut), there only if the sequences have two segments on
 // the average (16 of 64 tokens: 25 us cut, 19 not; of 32 heads of 128 x 128:
-// 81, 68).
+// 81, 68) or are the long ones of a batch of short ones (scan_split).
 struct ScanPlan {
   bool chunked;
   qs::ScanSegs segs;
@@ -236,11 +239,13 @@ static void set_pieces(const qs::ScanArgs& a, int64_t cut, ScanPlan* p) {
   p->total = (uint64_t)((a.T - 1) / cut + a.n) * (uint64_t)a.H * (uint64_t)(a.dv + a.dk) * (uint64_t)a.dk * 4u;
   p->uncut = (uint64_t)a.n * (uint64_t)a.H * 4u;
 }
+static bool chunks(const qs::ScanArgs& a) { return a.bf16 && !(a.key && a.delta); }
+// On the average, below 16 tokens (delta rule: 48, for its first launch) the
+// token by token kernel is ahead.
+static bool short_on_average(const qs::ScanArgs& a) { return a.T < (int64_t)a.n * (a.delta ? 48 : 16); }
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
-  // sequences' average length: below 16 tokens (delta rule: 48, for its first
-  // launch) the token by token kernel is ahead
-  p.chunked = a.bf16 && !(a.key && a.delta) && a.T >= (int64_t)a.n * (a.delta ? 48 : 16);
+  p.chunked = chunks(a) && (a.least > 0 || !short_on_average(a));
   p.segs.seg = 1 << 30;
   p.segs.count = a.n;
   if (a.delta && !p.chunked) {
@@ -274,7 +279,7 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   const int64_t work = (int64_t)a.T * a.H * ((a.dv + columns - 1) / columns);
   const int64_t least = !p.chunked ? 64 : a.key ? 128 : 256, groups = p.chunked && !a.key ? 512 : 1024;
   const int64_t seg = std::max<int64_t>(least, (work / groups + 63) / 64 * 64);
-  if (seg >= a.T || (!p.chunked && 2 * seg * a.n > a.T)) return p;
+  if (seg >= a.T || (!p.chunked && a.least == 0 && 2 * seg * a.n > a.T)) return p;
   p.segs.seg = (int32_t)seg;
   p.segs.count = (int32_t)((a.T + seg - 1) / seg + a.n);
   p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)a.dv * (uint64_t)a.dk * 4u;
@@ -283,11 +288,31 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
   return p;
 }
 
+// The average says nothing of a batch's longest sequence, which the host does not
+// know: many single tokens with one long prompt would go token by token, uncut.
+// So the sequences of this many tokens or more of a batch that is short on the
+// average go in launches of their own, as the plan for long ones says, and the
+// others token by token (0: no split).  Where there are none, those launches cost
+// about 5 ns for each head of a sequence; a token of a chain costs 0.2 us.  The
+// split is taken where one chain of all tokens would cost eight times the
+// launches.  32 heads of 128 x 64: 255 single tokens with a prompt of 2000 146 us,
+// 643 token by token; 256 of 8 tokens 139, 95.
+static int scan_split(const qs::ScanArgs& a) {
+  if (a.n < 2 || a.T < 1024 || (int64_t)a.n * a.H > (int64_t)a.T * 5) return 0;
+  if (chunks(a)) return short_on_average(a) ? 64 : 0;
+  if (a.delta) return 0;                       // pieces are of long sequences alone
+  qs::ScanArgs some = a;
+  some.least = 1;
+  const ScanPlan p = scan_plan(some);
+  return scan_plan(a).states || !p.states || 2 * p.segs.seg > a.T ? 0 : 2 * p.segs.seg;
+}
+
 qs_status qstate_scan_workspace(const qstate_handle* h, const qstate_scan_args* c, uint64_t* bytes) {
   if (!bytes) return op_fail(QS_EINVAL, "bytes is NULL");
   qs::ScanArgs a{};
   qs_status s = check_scan(h, c, &a);
   if (s != QS_OK) return s;
+  a.least = scan_split(a);
   const ScanPlan p = scan_plan(a);
   *bytes = p.states + p.total + p.uncut;
   return op_ok();
@@ -322,6 +347,7 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
     if (overlap(r, out) || overlap(r, fin)) return op_fail(QS_EINVAL, "an output overlaps an input");
   if (overlap(out, fin) || overlap(out, ini) || (c->initial != c->final && overlap(ini, fin)))
     return op_fail(QS_EINVAL, "an output overlaps another or the initial state");
+  const int split = a.least = scan_split(a);
   ScanPlan p = scan_plan(a);
   if (const uint64_t need = p.states + p.total + p.uncut) {
     if (!workspace || !aligned(workspace, 256) || bytes < need)
@@ -360,8 +386,10 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
   a.os = c->out_stride;
   const int64_t v = 16 / es;
   const int64_t far = int64_t(1) << 24;   // the kernels keep offsets within 64 rows in 32 bits
-  if (p.chunked && T > 1 && (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->out_stride > far))
-    return op_fail(QS_EUNSUPPORTED, "a stride of more than 2^24 elements");
+  if (p.chunked && T > 1 && (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->out_stride > far)) {
+    if (!split) return op_fail(QS_EUNSUPPORTED, "a stride of more than 2^24 elements");
+    a.most = -1;                               // token by token, all of them
+  }
   // Value rows of any width leave q and k their wide loads: 3080 tokens of 32 heads
   // of 256 x 35 by the delta rule 422 us, 957 with none; 3000 of 128 x 63,
   // additive: 73, 158.
@@ -370,9 +398,20 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
                   (T <= 1 || (c->v_stride % v == 0 && c->out_stride % v == 0));
   a.vec = !qk ? 0 : vo ? 2 : 1;
   if ((s = qs::op_check_device(h)) != QS_OK) return s;
-  hipError_t e = p.chunked ? (a.delta ? qs::launch_scan_delta : a.key ? qs::launch_scan_key : qs::launch_scan_chunk)(
-                                 a, p.segs, reinterpret_cast<hipStream_t>(stream))
-                           : qs::launch_scan(a, p.segs, reinterpret_cast<hipStream_t>(stream));
+  const hipStream_t on = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (split) {                                 // the short ones, in one piece each
+    qs::ScanArgs b = a;
+    b.least = 0;
+    b.most = a.most < 0 ? 0x7FFFFFFF : split - 1;
+    qs::ScanSegs whole{};
+    whole.seg = 1 << 30;
+    whole.count = a.n;
+    e = qs::launch_scan(b, whole, on);
+  }
+  if (e == hipSuccess && a.most >= 0)
+    e = (!p.chunked ? qs::launch_scan : a.delta ? qs::launch_scan_delta : a.key ? qs::launch_scan_key
+                                                                              : qs::launch_scan_chunk)(a, p.segs, on);
   if (e != hipSuccess) return op_fail(QS_EHIP, "scan launch: %s", hipGetErrorString(e));
   return op_ok();
 }

@@ -385,17 +385,26 @@ __global__ __launch_bounds__(64 * WAVES, DK <= 128 && VEC > 0 ? 2 : 1) void k_sc
 }
 
 // States between segments: for each sequence, S = initial, then S = decay S + local
-// from segment to segment; segment s's place takes the state before it.
+// from segment to segment; segment s's place takes the state before it.  Of the
+// long sequences alone there is at most one that begins in a cell of `least`
+// tokens, the last that does, so there are as many workgroups as cells need: one
+// for each short one that does nothing cost 40 us (256 of 32 heads of 128 x 64).
 __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanSegs g, int blocks) {
-  const int seq = (int)blockIdx.x / blocks;
+  int seq = (int)blockIdx.x / blocks;
+  if (a.least > 0) {
+    const int cell = seq;
+    seq = last_sequence(a, [&](int i) { return min(max(a.offsets[i], 0), a.T) / a.least <= cell; });
+    if (min(max(a.offsets[seq], 0), a.T) / a.least != cell) return;
+  }
   const int64_t per = (int64_t)a.dv * a.dk / 4, all = per * a.H;
   const int64_t e = (int64_t)((int)blockIdx.x % blocks) * 256 + threadIdx.x;
   if (e >= all) return;
   const int h = (int)(e / per);
   const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
-  if (end <= start) return;
+  if (end <= start || end - start < a.least || end - start > a.most) return;
   const int c0 = start / g.seg, c1 = (end - 1) / g.seg;
+  if (c0 == c1) return;                      // not cut
   bool numbers = true;
   F4* st = (F4*)g.states;
   F4 S = (F4){0, 0, 0, 0};
@@ -427,7 +436,7 @@ __global__ __launch_bounds__(256) void k_scan_join(const ScanArgs a, const ScanS
     }
   }
   if (!numbers) g.uncut[(int64_t)seq * a.H + h] = 1;
-  if (c1 > c0) st[(int64_t)(c1 + seq) * all + e] = S;
+  st[(int64_t)(c1 + seq) * all + e] = S;
 }
 
 template <int DK, int NV, int WAVES, int VEC>
@@ -452,7 +461,8 @@ hipError_t chunk_dk(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 
 hipError_t launch_scan_join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   const int blocks = (int)(((int64_t)a.H * a.dv * a.dk / 4 + 255) / 256);
-  k_scan_join<<<dim3((uint32_t)(a.n * blocks)), 256, 0, s>>>(a, g, blocks);
+  const int sequences = a.least > 0 ? a.T / a.least : a.n;
+  k_scan_join<<<dim3((uint32_t)(sequences * blocks)), 256, 0, s>>>(a, g, blocks);
   return hipGetLastError();
 }
 

@@ -537,7 +537,7 @@ __global__ __launch_bounds__(512) void k_delta_join(const ScanArgs a, const Scan
   const int h = hr / rchunks, r0 = hr % rchunks * kJoinRows;
   const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
-  if (!long_enough(start, end, cut)) return;
+  if (!long_enough(start, end, cut) || end - start < a.least || end - start > a.most) return;
   const int c0 = start / cut, c1 = (end - 1) / cut;
   auto piece_at = [&](int c) { return carry + ((int64_t)(c == c0 ? seq : a.n + c - 1) * a.H + h) * (a.dv + DK) * DK; };
   // this thread's elements of the rows, tid + 512 e, and its part of M: a channel, kJ rows

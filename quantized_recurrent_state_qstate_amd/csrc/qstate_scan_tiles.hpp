@@ -114,7 +114,7 @@ __device__ __forceinline__ Segment find_segment(const ScanArgs& a, int seg, int 
     end = min(max(a.offsets[r.seq + 1], start), a.T);
   }
   const int c = s - r.seq, c0 = start / seg, c1 = end > start ? (end - 1) / seg : c0;
-  r.none = c < c0 || c > c1;
+  r.none = c < c0 || c > c1 || end - start < a.least || end - start > a.most;
   r.first = c == c0;
   r.last = c == c1;
   r.t0 = r.first ? start : c * seg;
@@ -142,9 +142,9 @@ __device__ __forceinline__ Piece find_piece(const ScanArgs& a, int cut, int s) {
   const int seq = s < a.n ? s : a.offsets ? last_sequence(a, [&](int i) { return a.offsets[i] <= x; }) : 0;
   const int start = a.offsets ? min(max(a.offsets[seq], 0), a.T) : 0;
   const int end = a.offsets ? min(max(a.offsets[seq + 1], start), a.T) : a.T;
-  const bool many = long_enough(start, end, cut);
-  if (s < a.n) return {seq, start, many ? (start / cut + 1) * cut : end, true, !many, false, end};
-  return {seq, x, min(x + cut, end), false, x + cut >= end, !(many && start < x && x < end), end};
+  const bool many = long_enough(start, end, cut), none = end - start < a.least || end - start > a.most;
+  if (s < a.n) return {seq, start, many ? (start / cut + 1) * cut : end, true, !many, none, end};
+  return {seq, x, min(x + cut, end), false, x + cut >= end, none || !(many && start < x && x < end), end};
 }
 
 // A sequence that is cut needs its segments' whole decays (the delta rule's M) to

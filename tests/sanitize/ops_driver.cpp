@@ -234,6 +234,31 @@ int main() {
           CHECK(s == ((int64_t)n * 8 * (64 * 128 / 1024) < (1 << 24) ? QS_OK : QS_EUNSUPPORTED));
           CHECK(g_launches - before == (s == QS_OK));
         }
+        // many short sequences, of which one may be long: two parts, by length
+        {
+          const bool by_length = chunked || kind == QS_KIND_ADDITIVE;
+          for (int T : {600, 4095, 12000}) {
+            a = scan_args(c, T, 900, 4);
+            a.final = (float*)at(5000ull << 32);
+            a.initial = nullptr;
+            CHECK(qstate_scan_workspace(h, &a, &need) == QS_OK);
+            const int before = g_launches;
+            CHECK(qstate_scan(h, &a, need ? at(6000ull << 32) : nullptr, need, nullptr) == QS_OK);
+            const bool split = by_length && T > 600;
+            CHECK(g_launches - before == (split ? 2 : 1));
+            CHECK((g_chunked != 0) == (split && chunked) && (need > 0) == split);
+          }
+          if (chunked) {                              // rows too far apart for chunks: token by token, as in one part
+            a = scan_args(c, 12000, 900, 4);
+            a.final = (float*)at(5000ull << 32);
+            a.initial = nullptr;
+            a.q = at(1000ull << 32);
+            a.q_stride = (1 << 24) + 8;
+            const int before = g_launches;
+            CHECK(qstate_scan(h, &a, at(6000ull << 32), big, nullptr) == QS_OK);
+            CHECK(g_launches - before == 1 && g_chunked == 0);
+          }
+        }
         // slots
         qstate_sizes z;
         CHECK(qstate_plan(&c, &z) == QS_OK);
