@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from quantized_recurrent_state_qstate_amd import QState, StateConfig
-from test_gpu_scan_exact import DT, KINDS, U, inputs, remembered, roundings
+from test_gpu_scan_exact import DT, KINDS, bound, inputs, remembered, roundings
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -50,7 +50,7 @@ def test_each_sequence_as_by_itself(name, kind, decay, dtype, H, dk, dv):
         s = slice(int(start[i]), int(start[i + 1]))
         o, f = qs.scan(q[s], k[s], v[s], d[s], b[s], initial=S0[i:i + 1])
         size = o.float().square().mean(-1, keepdim=True).sqrt()
-        tol = 2 * 6 * 2 * U * no ** 0.5 * size + torch.finfo(DT[dtype]).eps * o.float().abs()
+        tol = 2 * 6 * bound(no) * size + torch.finfo(DT[dtype]).eps * o.float().abs()
         assert ((out[s].float() - o.float()).abs() <= tol).all(), f"sequence {i} of {L}"
-        assert (final[i] - f[0]).norm() <= 2 * 2 * U * ns ** 0.5 * f.norm(), f"state {i} of {L}"
+        assert (final[i] - f[0]).norm() <= 2 * bound(ns) * f.norm(), f"state {i} of {L}"
     qs.close()
