@@ -256,7 +256,9 @@ qs_status make_plan(const qstate_config* c, Plan* p) {
     return fail(QS_EUNSUPPORTED, "a head needs %u bytes of LDS staging (max %u)", p->lds, kMaxLds);
   const bool chunked = p->family == qs::kFamDense || p->family == qs::kFamKeymap;   // others: one group per head
   const uint64_t grid = BH * (chunked ? (uint64_t)p->row_chunks : 1u);
-  if (grid > 0x7FFFFFFFu) return fail(QS_EUNSUPPORTED, "B*H too large for one launch");
+  // a launch has fewer than 2^32 threads: the runtime takes the number modulo 2^32
+  if (grid > 0xFFFFFFFFull / (chunked ? (uint64_t)p->dense_threads : 256u))
+    return fail(QS_EUNSUPPORTED, "B*H too large for one launch");
   // the kernels form Philox block counters in 32 bits: element indices
   // B*H*dv*dk must stay below 2^35
   if (BH * (uint64_t)dv * (uint64_t)dk >= (1ull << 35))

@@ -229,3 +229,16 @@ def test_scale_axis_supported_set():
         with pytest.raises(_lib.QStateError) as e:
             plan(StateConfig(**kw))
         assert e.value.status == _lib.QS_EUNSUPPORTED, kw
+
+
+@pytest.mark.parametrize("kw,most", [
+    (dict(dk=64, dv=1), 2 ** 26 - 1),                                                    # 64 threads a head
+    (dict(dk=64, dv=4, lrb_rank=8, rounding="nearest"), 2 ** 24 - 1),                    # 256
+    (dict(dk=64, dv=4, scale_axis="head", rounding="nearest"), 2 ** 24 - 1),
+    (dict(dk=64, dv=4, H=1, map_mode="key", map=np.arange(64) < 8, qbits=8), 2 ** 24 - 1),
+])
+def test_a_step_has_fewer_than_two_to_the_32_threads(kw, most):
+    """The runtime takes a launch's threads modulo 2^32."""
+    plan(StateConfig(B=most, **kw))
+    with pytest.raises(_lib.QStateError, match="too large for one launch"):
+        plan(StateConfig(B=most + 1, **kw))
