@@ -224,6 +224,12 @@ def _empty_like(x, contiguous: bool, stream):
     return torch.empty_like(x)
 
 
+def check_stream(stream, device) -> None:
+    """A stream of the tensors' device, or None."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, expected {device}")
+
+
 def raw_stream(stream, device) -> int:
     """The hipStream_t of `stream`, or of the device's current stream."""
     if stream is not None:
@@ -366,6 +372,7 @@ class QState:
         import torch
         c = self.cfg
         dev = self.device
+        check_stream(stream, dev)
         ind = torch.bfloat16 if c.in_dtype == "bf16" else torch.float32
         if not isinstance(v, torch.Tensor) or v.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("k and v must be [T, heads, dim] tensors")
@@ -449,6 +456,7 @@ class QState:
         another element's source.  extra: up to 6 more tensors [B, ...] that
         go along (source_extra: theirs in the source)."""
         import torch
+        check_stream(stream, self.device)
         n = int(src_slot.numel())
         check_tensor("src_slot", src_slot, torch.int32, n, self.device)
         check_tensor("dst_slot", dst_slot, torch.int32, n, self.device)
@@ -477,6 +485,7 @@ class QState:
         [B, ...] that go along."""
         import torch
         c = self.cfg
+        check_stream(stream, self.device)
         if isinstance(live, torch.Tensor) and live.dtype == torch.bool:
             live = live.view(torch.uint8)
         check_tensor("live", live, torch.uint8, c.B, self.device)

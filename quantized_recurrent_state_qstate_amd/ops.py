@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .api import _empty_like, _ptr, check_rows, check_tensor, raw_stream
+from .api import _empty_like, _ptr, check_rows, check_stream, check_tensor, raw_stream
 
 
 def _device(name: str, x):
@@ -24,8 +24,6 @@ def _call(fn, name: str, args, device, stream) -> None:
     """Launch on `stream` (None: the device's current one) with the tensors' device current."""
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors on {device}, expected a GPU")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream on {stream.device}, expected {device}")
     import torch
     if device.index == torch._C._cuda_getDevice():
         status = fn(ctypes.byref(args), raw_stream(stream, device))
@@ -39,6 +37,7 @@ def _call(fn, name: str, args, device, stream) -> None:
 def _conv(x, weight, bias, window, slot, n, silu, out, stream):
     import torch
     dev = _device("x", x)
+    check_stream(stream, dev)
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [tokens, C] and weight [W, C]")
     (T, C), W = x.shape, weight.shape[0]
@@ -115,6 +114,7 @@ def qk_norm_rotate(q, k=None, *, norm="l2", q_weight=None, k_weight=None, eps=1e
     interleaved.  q_scale multiplies q_out.  q_out may be q, k_out may be k."""
     import torch
     dev = _device("q", q)
+    check_stream(stream, dev)
     if q.dim() != 3 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 3)):
         raise ValueError("q and k must be [T, heads, dim]")
     (T, hq, d), dtype = q.shape, q.dtype

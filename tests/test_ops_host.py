@@ -207,3 +207,20 @@ def test_windows_and_states_of_another_layout_are_refused():
         for shape in ((2, 4, 32, 64), (8, 32, 64), (2, 4, 2048), (2 * 4 * 32 * 64,), (1, 2, 4, 32, 64)):
             with pytest.raises(_lib.QStateError, match="handle is NULL"):    # as far as the library
                 qs.scan(**args, **{name: torch.zeros(shape)})
+
+
+def test_streams_of_another_device_are_refused():
+    """A stream is checked before anything is taken on it."""
+    from types import SimpleNamespace
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    qs = handle(B=2, H=4, dk=64, dv=32)
+    T, bf = 6, torch.bfloat16
+    idx, pool = torch.zeros(1, dtype=torch.int32), qs.new_state()
+    for call in (lambda: qs.scan(torch.zeros(T, 2, 64, dtype=bf), torch.zeros(T, 2, 64, dtype=bf),
+                                 torch.zeros(T, 4, 32, dtype=bf), torch.zeros(T, 4), stream=other),
+                 lambda: qs.copy_slots(pool, idx, idx, stream=other),
+                 lambda: qs.compact_slots(pool, torch.zeros(2, dtype=torch.uint8), stream=other),
+                 lambda: causal_conv(torch.zeros(T, 32), torch.zeros(4, 32), offsets=idx, stream=other),
+                 lambda: qk_norm_rotate(torch.zeros(T, 2, 64), stream=other)):
+        with pytest.raises(ValueError, match="stream on cuda:1, expected cpu"):
+            call()
