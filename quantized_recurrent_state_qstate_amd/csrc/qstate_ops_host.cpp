@@ -214,20 +214,21 @@ static qs_status check_scan(const qstate_handle* h, const qstate_scan_args* c, q
 
 // How a scan's sequences run (a.least > 0: the long ones of them).  The chunked
 // kernels take bf16 prompts but the delta rule with a decay for every key channel,
-// if the sequences are long enough on the average: one of 16 tokens, 32 heads of
-// 128 x 128, takes 7.4 us against 8.1 token by token (one of 8: 7.4, 6.1), sixteen
-// of 64 by the delta rule 71 against 90 us (of 32: 68, 50).  Everything else runs
-// token by token.
+// if the sequences are long enough on the average: of 32 tokens (32 heads of
+// 128 x 128: one 8.7 us, 9.9 token by token, sixteen 36, 41, 128 of them 221, 266;
+// of 16 tokens 8.6, 6.9, and 23, 26, and 217, 154), by the delta rule of 48 (sixteen
+// 60, 72; of 32 tokens one 15, 11, sixteen 47, 51).  Everything else runs token by
+// token.
 // Additive sequences are cut into segments when the heads alone would leave
 // compute units idle; a segment costs a state written, read and written again,
 // so it has at least 256 tokens (one decay a head; 16384 tokens of 32 heads of
-// 128 x 64: 140 us with segments for 512 workgroups, 155 us for 1024, 175 us
+// 128 x 64: 158 us with segments for 512 workgroups, 163 us for 1024, 200 us
 // for 384) or 128 (a decay a channel, whose blocks are slower; 2048 tokens of
-// 32 heads of 128 x 128: 118 us for 1024, 164 us with at least 256 tokens) or,
-// token by token, 64 (fp32, 2048 tokens of 8 heads of 64 x 64: 53 us, 62 with
-// at least 128, 464 uncut), there only if the sequences have two segments on
-// the average (16 of 64 tokens: 25 us cut, 19 not; of 32 heads of 128 x 128:
-// 81, 68) or are the long ones of a batch of short ones (scan_split).
+// 32 heads of 128 x 128: 107 us for 1024, 140 us with at least 256 tokens) or,
+// token by token, 64 (fp32, 2048 tokens of 8 heads of 64 x 64: 45 us, 43 with
+// at least 128, 285 uncut), there only if the sequences have two segments on
+// the average (16 of 64 tokens: 20 us cut, 13 not) or are the long ones of a batch
+// of short ones (scan_split).
 struct ScanPlan {
   bool chunked;
   qs::ScanSegs segs;
@@ -240,9 +241,8 @@ static void set_pieces(const qs::ScanArgs& a, int64_t cut, ScanPlan* p) {
   p->uncut = (uint64_t)a.n * (uint64_t)a.H * 4u;
 }
 static bool chunks(const qs::ScanArgs& a) { return a.bf16 && !(a.key && a.delta); }
-// On the average, below 16 tokens (delta rule: 48, for its first launch) the
-// token by token kernel is ahead.
-static bool short_on_average(const qs::ScanArgs& a) { return a.T < (int64_t)a.n * (a.delta ? 48 : 16); }
+// The token by token kernel is ahead.
+static bool short_on_average(const qs::ScanArgs& a) { return a.T < (int64_t)a.n * (a.delta ? 48 : 32); }
 static ScanPlan scan_plan(const qs::ScanArgs& a) {
   ScanPlan p{};
   p.chunked = chunks(a) && (a.least > 0 || !short_on_average(a));
@@ -253,8 +253,8 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     // Pieces: with up to 16384 rows at once a token costs little more than with
     // few; of 64 tokens or more (dk 256: 128), and at least four, as they go
     // twice.  fp32, one sequence: 1280 tokens of a head of 64 x 64 39 us, in one
-    // piece 196 (pieces of 128: 45); 5120 of 8 heads of 128 x 128 292, 944; 1280
-    // of 16 heads of 128 x 128 141, 239.  Every sequence has a place for L and M,
+    // piece 196 (pieces of 128: 45); 5120 of 8 heads of 128 x 128 301, 943; 1280
+    // of 16 heads of 128 x 128 140, 239.  Every sequence has a place for L and M,
     // so not with many (32768 rows of 256 are 34 MB).
     const int64_t cut = std::max<int64_t>(std::max(64, a.dk / 2), (a.T * rows / 16384 + 15) / 16 * 16);
     if (4 * rows <= 16384 && a.n * rows <= 32768 && a.T > 2 * cut) set_pieces(a, cut, &p);
@@ -265,13 +265,13 @@ static ScanPlan scan_plan(const qs::ScanArgs& a) {
     p.segs.count = (a.T + 63) / 64 + a.n;
     p.states = (uint64_t)p.segs.count * (uint64_t)a.H * (uint64_t)qs::kScanPrepBytes;
     // Pieces: as many as have their L and M made by 256 workgroups at once (the
-    // first needs no M, the last neither), of 512 tokens or more (dk 256: 1024; 4
-    // heads of 256 x 256, 2048 tokens: 210 us with 512, 187 in one piece).  One
-    // sequence of 8192 tokens: 2 heads of 128 x 128 105 us, in one piece 449; 8
-    // heads 146, 461; 32 heads 336, 513.  A batch with none that is long pays
-    // for launches that do nothing (8 of 1024 tokens, 16 heads: 103 us, 98).
+    // first needs no M, the last neither), of 512 tokens or more (4 heads of 256 x
+    // 256, 4096 tokens: 173 us, 217 with 1024).  One sequence of 8192 tokens of 128 x
+    // 128: 2 heads 112 us, in one piece 560; 8 heads 157, 573; 32 heads 375, 610.  A
+    // batch with none that is long pays for launches that do nothing (8 of 1024
+    // tokens, 16 heads: 125 us, 117).
     const int64_t wide = (a.dv + 63) / 64, blocks = (int64_t)a.H * (wide + a.dk / 64);   // of one piece's L and M
-    const int64_t cut = std::max<int64_t>(std::max(512, 4 * a.dk), (a.T / (256 / blocks + 1) + 63) / 64 * 64);
+    const int64_t cut = std::max<int64_t>(512, (a.T / (256 / blocks + 1) + 63) / 64 * 64);
     if (blocks <= 128 && a.n * a.H * wide <= 256 && a.T > 2 * cut) set_pieces(a, cut, &p);
     return p;
   }
@@ -391,8 +391,8 @@ qs_status qstate_scan(qstate_handle* h, const qstate_scan_args* c, void* workspa
     a.most = -1;                               // token by token, all of them
   }
   // Value rows of any width leave q and k their wide loads: 3080 tokens of 32 heads
-  // of 256 x 35 by the delta rule 422 us, 957 with none; 3000 of 128 x 63,
-  // additive: 73, 158.
+  // of 256 x 35 by the delta rule 481 us, 1026 with none; 3000 of 128 x 63,
+  // additive: 79, 152.
   const bool qk = aligned(c->q, 16) && aligned(c->k, 16) && (T <= 1 || (c->q_stride % v == 0 && c->k_stride % v == 0));
   const bool vo = aligned(c->v, 16) && aligned(c->out, 16) && a.dv % v == 0 &&
                   (T <= 1 || (c->v_stride % v == 0 && c->out_stride % v == 0));
