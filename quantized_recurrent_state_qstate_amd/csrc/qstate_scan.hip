@@ -12,13 +12,13 @@
 //
 // It carries fp32 prompts, short ones, and the delta rule with a decay a
 // channel.  Bound by the chain from token to token (a reduction in it by the
-// delta rule): about 0.19 us a token, 378 us for 2048 tokens of 8 heads of
-// 64 x 64 in one piece.  So long sequences are cut.  Additive: one pass for the
-// states that the segments add (no queries, no outputs), the join, one pass for
-// the outputs; 53 us against 464 uncut for the same sizes.  Delta rule, of few
-// heads: the first pass makes L and M of each piece, which maps the state before
-// it to S M + L (M's rows: the state's of an identity with values of zero);
-// 5120 tokens of 8 heads of 64 x 64: 119 us against 779.
+// delta rule): 0.15 us a token of 64 channels, 0.19 of 128; 315 us for 2048 tokens
+// of 8 heads of 64 x 64 in one piece.  So long sequences are cut.  Additive: one
+// pass for the states that the segments add (no queries, no outputs), the join,
+// one pass for the outputs; 45 us against 285 uncut for the same sizes.  Delta
+// rule, of few heads: the first pass makes L and M of each piece, which maps the
+// state before it to S M + L (M's rows: the state's of an identity with values of
+// zero); 5120 tokens of 8 heads of 64 x 64: 128 us against 780.
 #include <hip/hip_runtime.h>
 
 #include "qstate_scan_tiles.hpp"

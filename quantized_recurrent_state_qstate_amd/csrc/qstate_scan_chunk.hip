@@ -23,12 +23,13 @@
 // launches: the state each segment adds by itself, the states between
 // segments, and the outputs; so that few long sequences fill the device.
 //
-// 16384 tokens of 32 heads of 128 x 64 in 16 segments: 142 us, of which the local
-// states 39, the states between 12, the outputs 100.  The outputs' vector
-// instructions fill 35% of the time, matrix instructions 23%, LDS 49%: what is
-// left is waiting, with the two waves a SIMD that 60 KB of LDS and 206 registers
-// allow.  Chunks of 32 tokens (three waves) measured 145-149 us, with LDS rows
-// whose pieces are exchanged against bank conflicts the same 142.
+// 16384 tokens of 32 heads of 128 x 64 in 16 segments: 156 us.  Under a trace,
+// which makes them longer (171 in all), the local states take 41, the states
+// between 13, the outputs 117, of which vector instructions fill 30%, matrix
+// instructions 23%: what is left is LDS and waiting, with the two waves a SIMD that
+// 73 KB of LDS and 223 registers allow.  With outputs of two pieces, 142 us in all
+// then, chunks of 32 tokens (three waves) measured 145-149, and LDS rows whose
+// pieces are exchanged against bank conflicts the same 142.
 #include <hip/hip_runtime.h>
 
 #include "qstate_scan_tiles.hpp"

@@ -23,12 +23,13 @@
 //
 // Where few heads leave compute units idle, long sequences go in pieces at once:
 // a pass for what each piece does to the state before it, a short chain over
-// the pieces, a pass for the outputs.  One sequence of 8192 tokens, 32 heads of
-// 128 x 128, in 3 pieces: 57 us for the first launch, 125, 9 and 181 for the
-// others, 4.2 us a chunk at the outputs, of which 182 matrix instructions of a
-// wave (16 cycles each) are a third and their operands' splitting into pieces a
-// quarter, one after the other in the one wave a SIMD has; in one piece 513 us
-// in all.  2 heads, in 16 pieces: 105 us, in one 449.
+// the pieces, a pass for the outputs.  One sequence of 7868 tokens, 32 heads of
+// 128 x 128, in 3 pieces: 350 us; under a trace, which makes them longer (409 in
+// all), 55 for the first launch, 122, 12 and 220 for the others, 5.2 us a chunk at the
+// outputs, of which 216 matrix instructions of a wave (16 cycles each) are 28% and
+// 1190 vector instructions (4 cycles; most split operands into pieces) 38%, one
+// after the other in the one wave a SIMD has.  8192 tokens 375 us, in one piece
+// 610; of 2 heads, in 16 pieces, 112, in one 560.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -620,8 +621,8 @@ hipError_t join(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
 template <int DK, int VEC>
 hipError_t delta(const ScanArgs& a, const ScanSegs& g, hipStream_t s) {
   // 64 columns a workgroup: with 32, twice as many workgroups bring the same
-  // keys (one sequence of 7868 tokens, 32 heads of 128 x 128: 493 against 506 us
-  // in all; sixteen of 256: 107, 172).
+  // keys (measured with outputs of two pieces, in one piece a sequence: one of 7868
+  // tokens, 32 heads of 128 x 128: 493 against 506 us in all; sixteen of 256: 107, 172).
   constexpr int WAVES = 4;
   const int vchunks = (a.dv + 16 * WAVES - 1) / (16 * WAVES);
   k_delta_prep<DK, (VEC > 0)><<<dim3((uint32_t)(g.count * a.H)), 256, 0, s>>>(a, g.states, g.uncut);

@@ -21,10 +21,11 @@
 // A workgroup holds 64 NV value columns of one (segment, head), each wave 16 NV
 // in accumulators [dk][v].  Each wave prepares 4 of the block's 16 tokens.
 //
-// 2048 tokens of 32 heads of 128 x 128: 117 us, of which the local states 36, the
-// states between segments 12, the outputs 60.  Bound by vector instructions
-// (half of the outputs' time: cutting S into pieces every 16 tokens, and the
-// block's operands).
+// 2048 tokens of 32 heads of 128 x 128: 126 us with operands from HBM, 109 from the
+// Infinity Cache, of which (then, under a trace) the local states 34, the states
+// between segments 12, the outputs 73.  Vector instructions fill 32% of the
+// outputs' time (splitting S into pieces every 16 tokens, and the block's
+// operands), matrix instructions 19%; the rest is waiting, with two waves a SIMD.
 #include <hip/hip_runtime.h>
 
 #include "qstate_scan_tiles.hpp"
