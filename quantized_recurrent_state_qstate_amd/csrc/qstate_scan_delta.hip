@@ -24,10 +24,10 @@
 // Where few heads leave compute units idle, long sequences go in pieces at once:
 // a pass for what each piece does to the state before it, a short chain over
 // the pieces, a pass for the outputs.  One sequence of 7868 tokens, 32 heads of
-// 128 x 128, in 3 pieces: 350 us; under a trace, which makes them longer (409 in
-// all), 55 for the first launch, 122, 12 and 220 for the others, 5.2 us a chunk at the
-// outputs, of which 216 matrix instructions of a wave (16 cycles each) are 28% and
-// 1190 vector instructions (4 cycles; most split operands into pieces) 38%, one
+// 128 x 128, in 3 pieces: 350 us; under a trace, which makes them longer (422 in
+// all), 56 for the first launch, 127, 13 and 226 for the others, 5.5 us a chunk at the
+// outputs, of which 216 matrix instructions of a wave (16 cycles each) are 26% and
+// 1190 vector instructions (4 cycles; most split operands into pieces) 36%, one
 // after the other in the one wave a SIMD has.  8192 tokens 375 us, in one piece
 // 610; of 2 heads, in 16 pieces, 112, in one 560.
 #include <hip/hip_runtime.h>
